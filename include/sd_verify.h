@@ -17,6 +17,12 @@
  *   sd_linear        one dense projection of a few token rows with a normalising / gathering
  *                    prologue and a store, residual-add or gated-GELU epilogue (the drafter's
  *                    and the target's layers around their attention)
+ *   sd_rope          rotary positions of query or key rows (frequencies from sd_rope_freqs)
+ *   sd_append_kv     new K/V rows, one step's or whole prompts', into the paged cache, K and Q
+ *                    turned on the way; the cache in the rows' type or in 8 bits
+ *   sd_verify_attn_q8, sd_draft_xattn_q8
+ *                    the two attention calls over a cache held in 8 bits
+ *   sd_logprobs      log probability of given tokens, entropy and top alternatives
  *
  * Conventions shared by every call
  *   - Every data pointer is a caller-owned DEVICE buffer, densely packed in the layout
@@ -59,7 +65,9 @@ typedef enum {
   SD_ERR_DEVICE = 6       /* (status word) an out-of-range index met on the device */
 } sd_status;
 
-typedef enum { SD_F32 = 0, SD_BF16 = 1 } sd_dtype;
+/* SD_E4M3 (8-bit float: 4 exponent, 3 fraction bits, largest 448) only where a call names it:
+ * a cache written by sd_append_kv. */
+typedef enum { SD_F32 = 0, SD_BF16 = 1, SD_E4M3 = 2 } sd_dtype;
 
 /* ---------------------------------------------------------------------------------------
  * Attention over a paged KV cache.
@@ -350,6 +358,186 @@ size_t sd_linear_workspace_size(const sd_linear_desc *desc);
 sd_status sd_linear(const sd_linear_desc *desc, const void *x, const void *W, void *out,
                     const void *table, const int32_t *tokens, const int32_t *token_sel,
                     sd_stream stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Rotary positions.  The pages say nothing about positions; every decoder of the kind turns
+ * its queries and keys by the position before attention (Su et al., "RoFormer").
+ *
+ * Frequencies: sd_rope_freqs writes, for the rotating pair i < rot_dim / 2,
+ *     f_i = base^(-2 i / rot_dim)                                     SD_ROPE_PLAIN
+ *     f_i / factor                                                    SD_ROPE_LINEAR
+ *     f_i (g + (1 - g) / factor),                                     SD_ROPE_BY_PARTS
+ *       g = clamp((orig_ctx f_i / (2 pi) - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ *       (Peng et al., "YaRN")
+ * as a fraction of a turn in 64-bit fixed point, round(f_i / (2 pi) * 2^64): the angle of any
+ * int32 position modulo a turn is then one integer product, without rounding.  A program
+ * computes the table once and keeps it.  *amplitude (HOST, nullable) receives the factor on
+ * both cos and sin: 0.1 ln(factor) + 1 for SD_ROPE_BY_PARTS, else 1.
+ *   freqs   DEVICE uint64 [rot_dim / 2]
+ */
+typedef enum { SD_ROPE_HALF = 0, SD_ROPE_INTERLEAVED = 1 } sd_rope_layout;
+typedef enum { SD_ROPE_PLAIN = 0, SD_ROPE_LINEAR = 1, SD_ROPE_BY_PARTS = 2 } sd_rope_scaling;
+
+typedef struct {
+  int rot_dim;             /* rotating elements of a head: even, >= 2 */
+  double base;             /* > 1, e.g. 10000 */
+  sd_rope_scaling scaling;
+  double factor;           /* >= 1 (not PLAIN) */
+  int orig_ctx;            /* BY_PARTS: context the model was trained on */
+  double beta_fast;        /* BY_PARTS: turns over orig_ctx from which f_i is kept, e.g. 32 */
+  double beta_slow;        /* BY_PARTS: turns up to which f_i is divided, e.g. 1 */
+} sd_rope_freq_desc;
+
+sd_status sd_rope_freqs(const sd_rope_freq_desc *desc, uint64_t *freqs, float *amplitude,
+                        sd_stream stream);
+
+/* How a call turns a head: pair i is (x[i], x[i + rot_dim / 2]) for SD_ROPE_HALF and
+ * (x[2 i], x[2 i + 1]) for SD_ROPE_INTERLEAVED; at position t, with theta = t f_i,
+ *     (a, b) -> amplitude (a cos theta - b sin theta, b cos theta + a sin theta)
+ * in float32, rounded once to the row's type.  Elements from rot_dim on are left as they are. */
+typedef struct {
+  const uint64_t *freqs;   /* DEVICE [rot_dim / 2], from sd_rope_freqs */
+  int rot_dim;             /* even, <= head_dim */
+  sd_rope_layout layout;
+  float amplitude;
+} sd_rotary;
+
+/*
+ * sd_rope turns rows of `heads` heads, out of place or in place (out == x, ld_out == ld_x;
+ * otherwise the two must not overlap).
+ *   x    [rows, ld_x], the first heads * head_dim elements of a row        (f32 or bf16)
+ *   out  [rows, ld_out]
+ *   pos  int32 [rows], or NULL: row r sits at
+ *        ctx_len[r / rows_per_seq] + r % rows_per_seq + q_offset           (ctx_len int32)
+ * Any head_dim; rows of 16-byte aligned vectors (base, row strides, head_dim and the pairs'
+ * extent multiples of 16 bytes) take the vector path.  rows == 0 launches nothing.
+ */
+typedef struct {
+  int rows;
+  int heads;
+  int head_dim;
+  int64_t ld_x, ld_out;    /* row strides (elements) */
+  sd_dtype dtype;          /* element type of x and out: SD_F32 or SD_BF16 */
+  int rows_per_seq;        /* pos == NULL: rows of one sequence (k + 1) */
+  int q_offset;            /* pos == NULL: added to the position */
+} sd_rope_desc;
+
+sd_status sd_rope(const sd_rope_desc *desc, const sd_rotary *rot, const void *x,
+                  const int32_t *pos, const int32_t *ctx_len, void *out, sd_stream stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Append to the paged cache ("Gemma 4 MTP: drafter drafts, target verifies", section "drafter
+ * internal architecture": the cache that the target fills and the drafter reads too).
+ *
+ * Sequence b adds n_b rows, at positions ctx_len[b] .. ctx_len[b] + n_b - 1: rows b * n_new + j
+ * of k_new, v_new and q with n_b = n_new (cu_new == NULL), or rows cu_new[b] .. cu_new[b+1] - 1
+ * (prompts of different lengths packed one after another; n_b may be 0; rows from
+ * cu_new[batch] on are not read).  ctx_len is not advanced.
+ *   k_new, v_new [n_rows, ld], h_kv * head_dim elements of a row;  q [n_rows, ld_q] and
+ *   q_out [n_rows, ld_q_out], h_q * head_dim elements (h_q == 0: none; in place allowed)
+ *   k_cache, v_cache [num_blocks, h_kv, block_size, head_dim] of cache_dtype
+ *   block_table int32 [batch, max_blocks_per_seq], ctx_len int32 [batch],
+ *   cu_new int32 [batch + 1], not decreasing, from >= 0 to <= n_rows
+ * With rot != NULL the K and Q rows are turned by their position first (V never is).
+ *
+ * cache_dtype == dtype: the rows are stored as they are (turned rows rounded once).
+ *
+ * cache_dtype == SD_E4M3: element x of a block is held as the e4m3 value nearest to x / s
+ * (ties to even), s the block's scale of its kv head, k_scale for K and v_scale for V:
+ *     s = 2^e,  e = the smallest e >= -64 with |x| <= 448 2^e for the rows in question
+ *   - a call that writes row 0 of a block begins the block: s covers the rows it writes there;
+ *   - otherwise the block goes on: s becomes the larger of that and its former scale (positive
+ *     and finite, as left by this call), and when it grows the block's rows before the new ones
+ *     are rescaled in place.  Scales are powers of two, so only codes that become subnormal are
+ *     rounded a second time.  Rolled-back rows count until the block is begun again.
+ * Elements that are not finite do not count for s; infinities become +-448 s, NaN stays NaN.
+ *   k_scale, v_scale float32 [num_blocks, h_kv] (unused otherwise, NULL ok)
+ * Needs head_dim 64, 128, 256 or 512, block_size a multiple of 16, rot_dim a multiple of 16, all
+ * row pointers 16-byte aligned and row strides a multiple of 16 bytes.
+ *
+ * The destination blocks must be allocated in block_table, and no block may receive rows of two
+ * sequences in one call.  A block id out of range or a position beyond the table is skipped and
+ * recorded (SD_ERR_DEVICE).  No workspace.  n_rows == 0 launches nothing.
+ */
+typedef struct {
+  int batch;
+  int n_new;               /* rows of every sequence when cu_new == NULL (n_rows == batch * n_new) */
+  int n_rows;              /* rows of k_new, v_new and q */
+  int h_q, h_kv;           /* h_q == 0: no query rows */
+  int head_dim;
+  int block_size;
+  int max_blocks_per_seq;
+  int num_blocks;
+  int64_t ld_k, ld_v;      /* row strides (elements) */
+  int64_t ld_q, ld_q_out;
+  sd_dtype dtype;          /* of k_new, v_new, q, q_out: SD_F32 or SD_BF16 */
+  sd_dtype cache_dtype;    /* dtype or SD_E4M3 */
+} sd_append_desc;
+
+sd_status sd_append_kv(const sd_append_desc *desc, const sd_rotary *rot, const void *k_new,
+                       const void *v_new, const void *q, void *k_cache, void *v_cache,
+                       float *k_scale, float *v_scale, const int32_t *block_table,
+                       const int32_t *ctx_len, const int32_t *cu_new, void *q_out,
+                       sd_stream stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Attention over a cache held in 8 bits: sd_verify_attn and sd_draft_xattn with K_p and V_p the
+ * e4m3 rows of sd_append_kv times their block's scale.  Half the bytes of the bf16 calls.
+ *
+ * sd_verify_attn_q8: query j of sequence b sits at t = ctx_len[b] + j and attends to keys p in
+ * [lo, t], lo as for sd_verify_attn.  The n_q new rows must be in the cache already (one
+ * sd_append_kv before); the call reads the caches only.  sd_draft_xattn_q8: as sd_draft_xattn.
+ * desc->dtype must be SD_BF16, the type of q and out; head_dim 64, 128, 256 or 512, block_size a
+ * multiple of 16, (h_q / h_kv) * n_q <= 64.  Scales float32 [num_blocks, h_kv], >= 0 and finite
+ * (any such scales, not only powers of two).  All pointers but scales, tables and lengths
+ * 16-byte aligned.
+ *
+ * Scores are exact products of the bf16 query and the e4m3 keys, accumulated in float32; softmax
+ * weights enter the second product as two e4m3 parts (8 bits), relative to the largest of each
+ * 128 keys, and are accumulated in float32.  Key and value rows outside every query's range are
+ * not read as numbers (any codes may stand there).  A NaN in a V row that some, not all queries
+ * of the call attend to makes the whole output rows of those queries NaN.
+ */
+size_t sd_verify_attn_q8_workspace_size(const sd_attn_desc *desc);
+sd_status sd_verify_attn_q8(const sd_attn_desc *desc, const void *q, const void *k_cache,
+                            const void *v_cache, const float *k_scale, const float *v_scale,
+                            const int32_t *block_table, const int32_t *ctx_len, void *out,
+                            void *ws, size_t ws_bytes, sd_stream stream);
+size_t sd_draft_xattn_q8_workspace_size(const sd_attn_desc *desc);
+sd_status sd_draft_xattn_q8(const sd_attn_desc *desc, const void *q, const void *k_cache,
+                            const void *v_cache, const float *k_scale, const float *v_scale,
+                            const int32_t *block_table, const int32_t *ctx_len,
+                            const int32_t *q_pos, void *out, void *ws, size_t ws_bytes,
+                            sd_stream stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Log probabilities of given tokens (what a server answers beside the tokens that sd_accept
+ * emits): with x = logits[r] / temperature over the vocabulary, lse = ln sum_v exp(x_v),
+ *     logprob[r]         = x[tokens[r]] - lse
+ *     entropy[r]         = lse - sum_v p_v x_v,  p_v = exp(x_v - lse)          (nullable)
+ *     top_ids[r, i]      = the top_n most likely tokens, equal logits by lower id
+ *     top_logprobs[r, i] = x[top_ids[r, i]] - lse
+ * in float32.  Logits of -inf are tokens of probability 0 (log probability -inf, last among the
+ * alternatives).  A row whose token is negative (the padding of sd_accept's out_tokens) is not
+ * read: logprob and entropy 0, top_ids -1, top_logprobs -inf; a token >= vocab is treated the
+ * same and recorded (SD_ERR_DEVICE).  A row of nothing but -inf, or with a NaN or +inf, has NaN
+ * for every float output and -1 for every id.
+ *   logits float32 [rows, ld_logits], tokens int32 [rows], logprob, entropy float32 [rows],
+ *   top_ids int32 and top_logprobs float32 [rows, top_n] (NULL ok when top_n == 0)
+ * Workspace as for the other calls (no initialisation).
+ */
+typedef struct {
+  int rows;                /* 0: launches nothing */
+  int vocab;
+  int ld_logits;           /* floats between rows; 0 means vocab */
+  float temperature;       /* > 0 */
+  int top_n;               /* 0 .. 32, <= vocab */
+} sd_logprobs_desc;
+
+size_t sd_logprobs_workspace_size(const sd_logprobs_desc *desc);
+sd_status sd_logprobs(const sd_logprobs_desc *desc, const float *logits, const int32_t *tokens,
+                      float *logprob, float *entropy, int32_t *top_ids, float *top_logprobs,
+                      void *ws, size_t ws_bytes, sd_stream stream);
 
 /* ---------------------------------------------------------------------------------------
  * Status.

@@ -6,9 +6,12 @@ memory and streams.  There is no fallback: if the library is missing or a call f
 binding raises.
 
 Functions carry the C names (sd_verify_attn, sd_draft_xattn, sd_lm_head, sd_accept,
-sd_commit, sd_linear and the *_workspace_size / status helpers).  Tensors are passed as torch CUDA
+sd_commit, sd_linear, sd_rope, sd_append_kv, sd_verify_attn_q8, sd_draft_xattn_q8, sd_logprobs and
+the *_workspace_size / status helpers).  Tensors are passed as torch CUDA
 tensors (their data_ptr is used; they must be contiguous), descriptors as the ctypes
 structures below, ``stream`` as a torch.cuda.Stream (default: the current stream).
+Row tensors whose descriptor has a row stride (sd_rope, sd_append_kv) may be strided views whose
+rows are contiguous; a cache in 8 bits is a torch.float8_e4m3fn (or uint8) tensor.
 """
 from __future__ import annotations
 
@@ -22,7 +25,7 @@ LIB_PATH = os.path.join(_HERE, "libsdverify.so")
 
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_WORKSPACE = 0, 1, 2, 3
 SD_ERR_CUDA, SD_ERR_TIMEOUT, SD_ERR_DEVICE = 4, 5, 6
-SD_F32, SD_BF16 = 0, 1
+SD_F32, SD_BF16, SD_E4M3 = 0, 1, 2
 
 
 class SdError(RuntimeError):
@@ -82,6 +85,41 @@ class LinearDesc(ctypes.Structure):
                 ("ws", ctypes.c_void_p), ("ws_bytes", ctypes.c_size_t)]
 
 
+SD_ROPE_HALF, SD_ROPE_INTERLEAVED = 0, 1
+SD_ROPE_PLAIN, SD_ROPE_LINEAR, SD_ROPE_BY_PARTS = 0, 1, 2
+
+
+class RopeFreqDesc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("base", ctypes.c_double), ("scaling", ctypes.c_int),
+                ("factor", ctypes.c_double), ("orig_ctx", ctypes.c_int),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("ld_x", ctypes.c_int64), ("ld_out", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("rows_per_seq", ctypes.c_int), ("q_offset", ctypes.c_int)]
+
+
+class AppendDesc(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("n_new", ctypes.c_int), ("n_rows", ctypes.c_int),
+                ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("block_size", ctypes.c_int), ("max_blocks_per_seq", ctypes.c_int),
+                ("num_blocks", ctypes.c_int), ("ld_k", ctypes.c_int64), ("ld_v", ctypes.c_int64),
+                ("ld_q", ctypes.c_int64), ("ld_q_out", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("cache_dtype", ctypes.c_int)]
+
+
+class LogprobsDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("vocab", ctypes.c_int), ("ld_logits", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("top_n", ctypes.c_int)]
+
+
 _lib = None
 
 _P = ctypes.c_void_p
@@ -103,6 +141,21 @@ _SIGS = {
     "sd_commit": (ctypes.c_int, [ctypes.POINTER(CommitDesc), _P, _P, _P, _P, _P, _P, _P]),
     "sd_linear_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LinearDesc)]),
     "sd_linear": (ctypes.c_int, [ctypes.POINTER(LinearDesc), _P, _P, _P, _P, _P, _P, _P]),
+    "sd_rope_freqs": (ctypes.c_int, [ctypes.POINTER(RopeFreqDesc), _P,
+                                     ctypes.POINTER(ctypes.c_float), _P]),
+    "sd_rope": (ctypes.c_int, [ctypes.POINTER(RopeDesc), ctypes.POINTER(Rotary), _P, _P, _P, _P,
+                               _P]),
+    "sd_append_kv": (ctypes.c_int, [ctypes.POINTER(AppendDesc), ctypes.POINTER(Rotary)] +
+                     [_P] * 12),
+    "sd_verify_attn_q8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttnDesc)]),
+    "sd_verify_attn_q8": (ctypes.c_int, [ctypes.POINTER(AttnDesc)] + [_P] * 9 +
+                          [ctypes.c_size_t, _P]),
+    "sd_draft_xattn_q8_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttnDesc)]),
+    "sd_draft_xattn_q8": (ctypes.c_int, [ctypes.POINTER(AttnDesc)] + [_P] * 10 +
+                          [ctypes.c_size_t, _P]),
+    "sd_logprobs_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LogprobsDesc)]),
+    "sd_logprobs": (ctypes.c_int, [ctypes.POINTER(LogprobsDesc)] + [_P] * 7 +
+                    [ctypes.c_size_t, _P]),
     "sd_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sd_device_status_read": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int), _P]),
     "sd_device_status_clear": (ctypes.c_int, [_P]),
@@ -144,6 +197,25 @@ def _ptr(t):
         raise ValueError("tensor arguments must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_ptr(t, ld, rows, width):
+    """Address of row data [rows, ...] whose rows of ``width`` elements are contiguous and ``ld``
+    elements apart (a view of a wider buffer is fine)."""
+    if t is None or isinstance(t, int):
+        return t
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must live on a CUDA device")
+    if t.is_contiguous() and t.numel() >= (rows - 1) * ld + width:
+        return t.data_ptr()
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != inner:
+            raise ValueError("a row's elements must be contiguous")
+        inner *= n
+    if inner < width or t.shape[0] < rows or (rows > 1 and t.stride(0) != ld):
+        raise ValueError("row tensor does not fit the descriptor's rows, width and row stride")
     return t.data_ptr()
 
 
@@ -236,6 +308,76 @@ def sd_linear(desc, x, w, out, table=None, tokens=None, token_sel=None, stream=N
     _check("sd_linear", lib().sd_linear(
         ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(out), _ptr(table), _ptr(tokens),
         _ptr(token_sel), _stream(stream)))
+
+
+def sd_rope_freqs(desc, freqs, stream=None) -> float:
+    """Fills ``freqs`` (int64 [rot_dim / 2]: 64-bit fractions of a turn) and returns the amplitude."""
+    amp = ctypes.c_float(1.0)
+    _check("sd_rope_freqs", lib().sd_rope_freqs(ctypes.byref(desc), _ptr(freqs), ctypes.byref(amp),
+                                                _stream(stream)))
+    return amp.value
+
+
+def rotary(freqs, layout=SD_ROPE_HALF, amplitude=1.0) -> Rotary:
+    """The rotation argument of sd_rope and sd_append_kv; it keeps ``freqs`` alive."""
+    r = Rotary(_ptr(freqs), 2 * freqs.numel(), layout, amplitude)
+    r.table = freqs
+    return r
+
+
+def _ref(x):
+    return ctypes.byref(x) if x is not None else None
+
+
+def sd_rope(desc, rot, x, pos, ctx_len, out, stream=None):
+    width = desc.heads * desc.head_dim
+    _check("sd_rope", lib().sd_rope(
+        ctypes.byref(desc), _ref(rot), _rows_ptr(x, desc.ld_x, desc.rows, width), _ptr(pos),
+        _ptr(ctx_len), _rows_ptr(out, desc.ld_out, desc.rows, width), _stream(stream)))
+
+
+def sd_append_kv(desc, rot, k_new, v_new, q, k_cache, v_cache, k_scale, v_scale, block_table,
+                 ctx_len, cu_new=None, q_out=None, stream=None):
+    n, kv, w = desc.n_rows, desc.h_kv * desc.head_dim, desc.h_q * desc.head_dim
+    _check("sd_append_kv", lib().sd_append_kv(
+        ctypes.byref(desc), _ref(rot), _rows_ptr(k_new, desc.ld_k, n, kv),
+        _rows_ptr(v_new, desc.ld_v, n, kv), _rows_ptr(q, desc.ld_q, n, w), _ptr(k_cache),
+        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(ctx_len),
+        _ptr(cu_new), _rows_ptr(q_out, desc.ld_q_out, n, w), _stream(stream)))
+
+
+def sd_verify_attn_q8_workspace_size(desc: AttnDesc) -> int:
+    return lib().sd_verify_attn_q8_workspace_size(ctypes.byref(desc))
+
+
+def sd_verify_attn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, out, ws,
+                      stream=None):
+    _check("sd_verify_attn_q8", lib().sd_verify_attn_q8(
+        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_table), _ptr(ctx_len), _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def sd_draft_xattn_q8_workspace_size(desc: AttnDesc) -> int:
+    return lib().sd_draft_xattn_q8_workspace_size(ctypes.byref(desc))
+
+
+def sd_draft_xattn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, q_pos,
+                      out, ws, stream=None):
+    _check("sd_draft_xattn_q8", lib().sd_draft_xattn_q8(
+        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+        _ptr(block_table), _ptr(ctx_len), _ptr(q_pos), _ptr(out), _ptr(ws), _nbytes(ws),
+        _stream(stream)))
+
+
+def sd_logprobs_workspace_size(desc: LogprobsDesc) -> int:
+    return lib().sd_logprobs_workspace_size(ctypes.byref(desc))
+
+
+def sd_logprobs(desc, logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None,
+                ws=None, stream=None):
+    _check("sd_logprobs", lib().sd_logprobs(
+        ctypes.byref(desc), _ptr(logits), _ptr(tokens), _ptr(logprob), _ptr(entropy),
+        _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def sd_device_status_read(stream=None) -> int:

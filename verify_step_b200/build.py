@@ -20,7 +20,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsdverify.so")
-SOURCES = ["abi.cu", "attention.cu", "lm_head.cu", "accept.cu", "commit.cu", "linear.cu"]
+SOURCES = ["abi.cu", "attention.cu", "lm_head.cu", "accept.cu", "commit.cu", "linear.cu",
+           "kv_append.cu", "attn_q8.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xcompiler", "-Wall", "-Xcompiler", "-Wno-unused-function"]

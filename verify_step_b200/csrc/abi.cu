@@ -137,6 +137,21 @@ bool encode_tmap_kv_chunks_bf16(CUtensorMap *map, const void *base, uint64_t D, 
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_kv_bytes(CUtensorMap *map, const void *base, uint64_t D, uint64_t rows,
+                          uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t inner = D < 128 ? D : 128;
+  const cuuint64_t dims[4] = {inner, 8, D / inner, rows / 8};
+  const cuuint64_t strides[3] = {D, inner, D * 8};
+  const cuuint32_t box[4] = {(cuuint32_t)inner, 8, (cuuint32_t)(D / inner), box_rows / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            inner == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace sdv
 
 extern "C" {

@@ -47,6 +47,13 @@ bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t inner, uin
 bool encode_tmap_kv_chunks_bf16(CUtensorMap *map, const void *base, uint64_t D, uint64_t rows,
                                 uint32_t box_rows);
 
+// A [rows x D] matrix of bytes viewed as (min(D, 128) bytes, 8 rows, D / 128 chunks, rows / 8), so
+// that one 4D box of box_rows rows arrives as 8-row groups of whole swizzled chunks: [group][chunk]
+// [8 rows][128 bytes], the uniform group stride that a matrix descriptor needs.  128-byte swizzle
+// (64-byte at D 64).  rows and box_rows multiples of 8.
+bool encode_tmap_kv_bytes(CUtensorMap *map, const void *base, uint64_t D, uint64_t rows,
+                          uint32_t box_rows);
+
 inline sd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? SD_OK : SD_ERR_CUDA; }
 
 // Programmatic dependent launch: off unless the environment sets SDV_PDL=1 (read once per

@@ -369,8 +369,8 @@ sd_status sd_linear(const sd_linear_desc *desc, const void *x, const void *W, vo
  *     f_i (g + (1 - g) / factor),                                     SD_ROPE_BY_PARTS
  *       g = clamp((orig_ctx f_i / (2 pi) - beta_slow) / (beta_fast - beta_slow), 0, 1)
  *       (Peng et al., "YaRN")
- * as a fraction of a turn in 64-bit fixed point, round(f_i / (2 pi) * 2^64): the angle of any
- * int32 position modulo a turn is then one integer product, without rounding.  A program
+ * (f_i in float64) as a fraction of a turn in 64-bit fixed point, round(f_i / (2 pi) * 2^64): the
+ * angle of any int32 position modulo a turn is then one integer product, without rounding.  A program
  * computes the table once and keeps it.  *amplitude (HOST, nullable) receives the factor on
  * both cos and sin: 0.1 ln(factor) + 1 for SD_ROPE_BY_PARTS, else 1.
  *   freqs   DEVICE uint64 [rot_dim / 2]

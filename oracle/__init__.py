@@ -14,9 +14,13 @@ Modules
   commit     committed length, committed slots, rollback and next hidden row
   drafter    the drafter's dense layers around its cross-attention (one link of the chain)
   target     the target's layers over the k+1 verified positions (multi-layer verify)
+  rotary     rotary positions (half and interleaved, part of the head, stretched contexts)
+  kv8        the paged cache in e4m3 with power-of-two block scales
+  logprobs   log probabilities of given tokens, entropy and top alternatives
 
 Parity status: every function is pinned by tests/test_oracle_*.py against closed forms,
 invariants, library routines, brute-force enumeration or published known answers, except
 agreement with real Gemma 4 / vLLM / FlashInfer outputs (no weights or traces exist here).
 """
-from . import accept, attention, commit, drafter, lm_head, philox, target  # noqa: F401
+from . import (accept, attention, commit, drafter, kv8, lm_head, logprobs, philox,  # noqa: F401
+               rotary, target)

@@ -656,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float tm = sm.red[buf][0][lane];
 #pragma unroll
         for (int q = 1; q < 4; ++q) tm = fmaxf(tm, sm.red[buf][q][lane]);
+        if (tm != tm) tm = 0.f;  // nothing but NaN: the weights are, and l and O become NaN
         const float m_new = fmaxf(m_run, tm);
         const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
         const float beta = tm == -INFINITY ? 0.f : ex2_approx(tm - m_new) * 0x1p-8f;

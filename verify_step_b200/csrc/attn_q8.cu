@@ -34,8 +34,10 @@ namespace sdv {
 namespace q8 {
 
 constexpr int kTile = 128;  // keys
-constexpr int kThreads = 384;
 constexpr int kScaleRing = 4;
+// Score tiles computed ahead of the output products: V of a tile is then loaded when its weights
+// are nearly done, so it does not hold a ring slot through the softmax.
+constexpr int kAhead = 2;
 
 struct Params {
   int B, n_q, Hq, Hkv, G, D, bs, mbps, num_blocks, window, M;
@@ -80,13 +82,23 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
   return s;
 }
 
-// Last key of query row r (row j * G + h) and its first one.
-__device__ __forceinline__ int row_hi(const Params &p, const Seq &s, int row) {
-  return p.is_draft ? s.hi : s.t0 + row / p.G;
+// Last key of query j (row j * G + h) and its first one.
+__device__ __forceinline__ int row_hi(const Params &p, const Seq &s, int j) {
+  return p.is_draft ? s.hi : s.t0 + j;
 }
-__device__ __forceinline__ int row_lo(const Params &p, const Seq &s, int row) {
-  const int t = p.is_draft ? s.t0 : s.t0 + row / p.G;
+__device__ __forceinline__ int row_lo(const Params &p, const Seq &s, int j) {
+  const int t = s.t0 + j;
   return p.window > 0 ? max(0, t - p.window + 1) : 0;
+}
+
+// First tile of share c of P (P <= total): the shares differ by at most one tile.
+__host__ __device__ __forceinline__ unsigned share(unsigned total, unsigned c, unsigned P) {
+  return total / P * c + min(total % P, c);
+}
+// The share that holds tile x.
+__device__ __forceinline__ unsigned share_of(unsigned total, unsigned x, unsigned P) {
+  const unsigned q = total / P, r = total % P;
+  return x < (q + 1) * r ? x / (q + 1) : r + (x - (q + 1) * r) / q;
 }
 
 // A CTA's share of the flattened list: where it begins.
@@ -129,30 +141,41 @@ struct Cfg {
   static constexpr int MT = D >= 128 ? D / 128 : 1;   // 128-column chunks of the output
   static constexpr int RB = D >= 128 ? 128 : 64;      // bytes of a swizzled row
   static constexpr int CH = D / RB;                   // chunks of a row
+  // Eight rows a softmax warpgroup and at most 48 accumulators a joining thread: the code of a
+  // role is short (the instruction cache of a GPC is shared by its SMs: with 16 rows a thread the
+  // tile time differed by 1.3x between GPCs of 16 and 20 SMs) and no register spills.
+  static constexpr int SG = NR / 8;
+  static constexpr int MJ = MT * NR <= 48 ? MT : MT / 2 * NR <= 48 ? MT / 2 : 1;
+  static constexpr int JG = MT / MJ;                  // joining warpgroups, MJ chunks each
+  static constexpr int THREADS = 128 * (1 + SG + JG);
   static constexpr int SLOT = kTile * D;
   static constexpr int NQ = D == 512 ? 1 : 2;         // query buffers
   static constexpr int NP = D == 512 && NR == 24 ? 1 : 2;  // weight buffers
+  static constexpr int NO = D == 512 && NR == 24 ? 1 : 2;  // output tile buffers
+  static constexpr int NS = kAhead + 1;               // score buffers
   static constexpr int QBYTES = N2 * D;
   static constexpr int PBYTES = N2 * kTile;
-  static constexpr int S_COL = 0;                     // two score buffers
-  static constexpr int O_COL = 2 * N2;                // two output tiles
-  static constexpr int COLS = 2 * N2 + 2 * MT * N2;
+  static constexpr int S_COL = 0;
+  static constexpr int O_COL = NS * N2;
+  static constexpr int COLS = NS * N2 + NO * MT * N2;
   static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128
                                    : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
   struct Small {
     float scales[kScaleRing][2][8];
-    float red[2][4][NR];
-    float row[4][3][NR];  // per softmax warp: tile max - 8, alpha, beta
-    float2 ab[4][NR];     // alpha, beta for the joining warps
-    float2 ml[2][NR];    // m, l of an item
-    float qs[2][NR];     // 2^e scale of the query rows
+    float red[SG][2][4][8];
+    float row[4 * SG][3][8];  // per softmax warp: tile max - 8, alpha, beta
+    float2 ab[4][NR];         // alpha, beta for the joining warps
+    float2 ml[2][NR];         // m, l of an item
+    float qs[2][NR];          // 2^e scale of the query rows
+    int rowj[NR];             // query position of a row (row / G)
     uint64_t full[8], empty[8];
     uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
-    uint64_t qfull[2], qempty[2], sfull[2], sempty[2], pfull[2], pempty[2], ofull[2], oempty[2],
+    uint64_t qfull[2], qempty[2], sfull[NS], sempty[NS], pfull[2], pempty[2], ofull[2], oempty[2],
         lfull[2], lempty[2], abfull[4], drain;
     Start start;
     uint32_t tmem;
+    int hole[kScaleRing];     // a block of the tile does not exist
     int abort_flag;
   };
   static constexpr int FIXED = 1024 + NQ * QBYTES + NP * PBYTES + (int)sizeof(Small);
@@ -232,22 +255,61 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
   lo = e4m3x2((x - h.x) * 16.f, (y - h.y) * 16.f);
 }
 
+// 32 lanes x 8 columns: thread i of the warp gets lane (base + i).
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ float redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
 
-// Barrier of the 128 softmax threads that also tells whether any of them failed a wait.
-__device__ __forceinline__ bool softmax_barrier(bool fail) {
+// mbar_wait that sleeps in the hardware between tries: a spinning warp takes issue slots from the
+// warps that compute (B 8 verify at D 512: 157 us spinning).
+__device__ __forceinline__ bool try_wait_hint(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  unsigned long long t0 = 0;
+  while (!try_wait_hint(bar, parity)) {
+    const unsigned long long now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > kWaitLimitNs) return false;
+  }
+  return true;
+}
+
+// One arrival for the warp, once all its lanes are here (32 arrivals on one address serialise).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// Barrier ``id`` of ``n`` threads that also tells whether any of them failed a wait.
+__device__ __forceinline__ bool barrier_or(int id, int n, bool fail) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)fail)
+      : "r"((uint32_t)fail), "r"(id), "r"(n)
       : "memory");
   return r != 0;
 }
@@ -261,11 +323,12 @@ __device__ __forceinline__ uint32_t tile_byte(int rows, int row, int col) {
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     attn_q8_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
   using C = Cfg<D, NR>;
-  constexpr int N2 = C::N2, MT = C::MT, RB = C::RB, SLOTS = C::SLOTS, NQ = C::NQ, NP = C::NP;
+  constexpr int N2 = C::N2, MT = C::MT, RB = C::RB, SLOTS = C::SLOTS, NQ = C::NQ, NP = C::NP,
+                NO = C::NO, NS = C::NS, SG = C::SG, JG = C::JG, MJ = C::MJ;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -278,28 +341,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x / p.R, rg = blockIdx.x % p.R;  // share of the list, row group
   const int row0 = rg * p.RG;
+  const int rows = min(p.RG, p.M - row0);  // rows of this group
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&sm.sc_full[i], 16);
-      mbar_init(&sm.sc_empty[i], 128);
+      mbar_init(&sm.sc_full[i], 16 + 1);
+      mbar_init(&sm.sc_empty[i], 4 * SG);
+    }
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm.sfull[i], 1);
+      mbar_init(&sm.sempty[i], 4 * SG);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.qfull[i], 64);
-      mbar_init(&sm.qempty[i], 1 + 4);  // the item's last scores; its row scales are read
-      mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.sempty[i], 128);
-      mbar_init(&sm.pfull[i], 128);
+      mbar_init(&sm.qfull[i], 2);
+      mbar_init(&sm.qempty[i], 1 + 4 * SG);  // the item's last scores; its row scales are read
+      mbar_init(&sm.pfull[i], 4 * SG);
       mbar_init(&sm.pempty[i], 1);
       mbar_init(&sm.ofull[i], 1);
-      mbar_init(&sm.oempty[i], 128);
-      mbar_init(&sm.lfull[i], 128);
-      mbar_init(&sm.lempty[i], 128);
+      mbar_init(&sm.oempty[i], 4 * JG);
+      mbar_init(&sm.lfull[i], 4 * SG);
+      mbar_init(&sm.lempty[i], 4 * JG);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sm.abfull[i], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.abfull[i], SG);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -308,34 +374,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&sm.tmem, C::TMEM);
     tmem_relinquish();
   }
+  if (warp == 2 && lane < NR) sm.rowj[lane] = (row0 + min(lane, rows - 1)) / p.G;
   pdl_trigger();
   pdl_wait();
   if (warp == 0) {
     // where this CTA's share of the T tiles begins
-    long long total = 0;
+    unsigned total = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
-      int n = b < p.B ? seq_of(p, b, blockIdx.x == 0).n : 0;
-      n = __reduce_add_sync(0xffffffffu, n);
-      total += (long long)n * p.Hkv;
+      const unsigned n = b < p.B ? seq_of(p, b, blockIdx.x == 0).n : 0;
+      total += __reduce_add_sync(0xffffffffu, n) * p.Hkv;
     }
-    const long long at = total * cta / p.P, end = total * (cta + 1) / p.P;
-    Start st{0, 0, 0, (int)(end - at)};
-    long long pre = 0;
+    const unsigned P = min((unsigned)p.P, total);
+    Start st{0, 0, 0, 0};
+    unsigned at = 0;
+    if ((unsigned)cta < P) {
+      at = share(total, cta, P);
+      st.left = (int)(share(total, cta + 1, P) - at);
+    }
+    unsigned pre = 0;
     for (int b0 = 0; b0 < p.B && st.left > 0; b0 += 32) {
       const int b = b0 + lane;
-      const int n = b < p.B ? seq_of(p, b, false).n : 0;
-      long long v = (long long)n * p.Hkv;
+      const unsigned n = b < p.B ? seq_of(p, b, false).n : 0;
+      unsigned v = n * p.Hkv;
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
       }
-      const bool here = at < pre + v;
-      const unsigned m = __ballot_sync(0xffffffffu, here);
+      const unsigned m = __ballot_sync(0xffffffffu, at < pre + v);
       if (m) {
         const int src = __ffs(m) - 1;
-        const long long before = pre + __shfl_sync(0xffffffffu, v - (long long)n * p.Hkv, src);
-        const int nn = __shfl_sync(0xffffffffu, n, src);
+        const unsigned before = pre + __shfl_sync(0xffffffffu, v - n * p.Hkv, src);
+        const unsigned nn = __shfl_sync(0xffffffffu, n, src);
         st.b = b0 + src;
         st.g = (int)((at - before) / nn);
         st.tau = (int)((at - before) % nn);
@@ -354,24 +424,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     record_status(p.status, SD_ERR_TIMEOUT);
     *abort_flag = 1;
   };
+  Walk w;
+  w.begin(p, st);
 
   if (warp == 0) {
     // -------------------------------------------------------------------- TMA producer
-    // Ring order K0, K1, V0, K2, V1, ... (the order in which the products need the tiles).
+    // Ring order K0 .. K_ahead, V0, K, V1, ...: the order in which the products need the tiles.
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     const uint64_t policy = l2_policy_evict_first();
-    Walk w;
-    w.begin(p, st);
     uint32_t it = 0;
     bool ok = true;
     const int boxes = kTile / p.bk, per_blk = p.bs / p.bk;
-    // the previous tile's V boxes: lane i holds its i-th box
-    int v_row = -1, v_boxes = 0;
-    bool pending = false;
+    int v_row[kAhead + 1], v_boxes[kAhead + 1];  // boxes of the last tiles: lane i holds its i-th
     auto load_slot = [&](const CUtensorMap *map, int row, uint32_t bytes) {
       const int slot = it % SLOTS;
-      const bool free = mbar_wait(&sm.empty[slot], ((it / SLOTS) & 1) ^ 1, abort_flag);
+      const bool free = wait_for(&sm.empty[slot], ((it / SLOTS) & 1) ^ 1, abort_flag);
       if (!__all_sync(0xffffffffu, free)) {
         if (lane == 0) fail();
         return false;
@@ -384,32 +452,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
       return true;
     };
-    for (int i = 0; w.left > 0 || pending; ++i) {
+    for (int i = 0; i < st.left + kAhead; ++i) {
       int row = -1, nb = 0;
-      const bool have = w.left > 0;
-      if (have) {
-        const int p0 = w.pos();
-        // lane's box of this tile and, for the scales, lane & 7's group of 16 keys
-        const int pk = p0 + lane * p.bk;
+      if (i < st.left) {
+        const int pk = w.pos() + lane * p.bk;  // lane's box
+        bool hole = false;
         if (lane < boxes && pk <= w.s.hi) {
           const int blk = p.table[(size_t)w.b * p.mbps + pk / p.bs];
           if (blk >= 0 && blk < p.num_blocks)
             row = (blk * p.Hkv + w.g) * p.bs + (pk / p.bk % per_blk) * p.bk;
           else
-            record_status(p.status, SD_ERR_DEVICE);
+            hole = true;
         }
-        const unsigned got = __ballot_sync(0xffffffffu, row >= 0);
-        nb = __popc(got);
+        nb = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        hole = __any_sync(0xffffffffu, hole);
         const int r = i % kScaleRing;
-        ok = mbar_wait(&sm.sc_empty[r], ((i / kScaleRing) & 1) ^ 1, abort_flag);
+        ok = wait_for(&sm.sc_empty[r], ((i / kScaleRing) & 1) ^ 1, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) {
           if (lane == 0) fail();
           break;
         }
+        if (lane == 0) {
+          if (hole) record_status(p.status, SD_ERR_DEVICE);
+          sm.hole[r] = hole;
+          mbar_arrive(&sm.sc_full[r]);
+        }
+        // scales of the 16-key group lane & 7
         const int grp = lane & 7;
-        const int src = grp * 16 / p.bk;  // the box that holds the group
-        const int srow = __shfl_sync(0xffffffffu, row, src);
+        const int srow = __shfl_sync(0xffffffffu, row, grp * 16 / p.bk);
         if (lane < 16) {
           float *dst = &sm.scales[r][lane >> 3][grp];
           if (srow >= 0) {
@@ -422,15 +493,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ok = load_slot(&kmap, row, nb * p.box_bytes);
         if (!ok) break;
+        w.next(p);
       }
-      if (pending) {
-        ok = load_slot(&vmap, v_row, v_boxes * p.box_bytes);
+#pragma unroll
+      for (int k = kAhead; k > 0; --k) {
+        v_row[k] = v_row[k - 1];
+        v_boxes[k] = v_boxes[k - 1];
+      }
+      v_row[0] = row;
+      v_boxes[0] = nb;
+      if (i >= kAhead) {
+        ok = load_slot(&vmap, v_row[kAhead], v_boxes[kAhead] * p.box_bytes);
         if (!ok) break;
       }
-      pending = have;
-      v_row = row;
-      v_boxes = nb;
-      if (have) w.next(p);
     }
     if (!ok && lane == 0)
       for (uint32_t j = it > (uint32_t)SLOTS ? it - SLOTS : 0; j < it; ++j)
@@ -441,66 +516,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_f8(128, N2, false), id_o = idesc_f8(128, N2, true);
       const uint32_t s0 = smem_u32(slots), q0 = smem_u32(qbuf), pb0 = smem_u32(pbuf);
-      Walk w;
-      w.begin(p, st);
       uint32_t it = 0, items = 0;
-      bool ok = true;
-      // scores of tile i (the walk stands on it)
-      auto scores = [&](int i) {
-        const int slot = it % SLOTS, buf = i & 1;
-        if (w.first(st)) {
-          if (!mbar_wait(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag)) return false;
-          ++items;
-        }
-        const uint32_t qb = q0 + ((items - 1) % NQ) * C::QBYTES;
-        if (!mbar_wait(&sm.full[slot], (it / SLOTS) & 1, abort_flag)) return false;
-        if (!mbar_wait(&sm.sempty[buf], ((i >> 1) & 1) ^ 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t a = s0 + slot * C::SLOT;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          const uint32_t ch = k * 32 / RB, x = k * 32 % RB;
-          umma_f8(tmem + C::S_COL + buf * N2, smem_desc<RB>(a + ch * 8 * RB + x, D * 8, 1),
-                  smem_desc<RB>(qb + ch * N2 * RB + x, RB * 8, 1), id_s, k > 0);
-        }
-        umma_commit(&sm.sfull[buf]);
-        umma_commit(&sm.empty[slot]);
-        if (w.last()) umma_commit(&sm.qempty[(items - 1) % NQ]);
-        ++it;
-        return true;
-      };
-      auto outputs = [&](int i) {
-        const int slot = it % SLOTS, buf = i & 1;
-        if (!mbar_wait(&sm.full[slot], (it / SLOTS) & 1, abort_flag)) return false;
-        if (!mbar_wait(&sm.pfull[i % NP], (i / NP) & 1, abort_flag)) return false;
-        if (!mbar_wait(&sm.oempty[buf], ((i >> 1) & 1) ^ 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t a = s0 + slot * C::SLOT, b = pb0 + (i % NP) * C::PBYTES;
-#pragma unroll
-        for (int c = 0; c < MT; ++c)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f8(tmem + C::O_COL + (buf * MT + c) * N2,
-                    smem_desc<RB>(a + c * 8 * RB + k * 4 * D * 8, D * 8, 0),
-                    smem_desc<128>(b + k * 32, 1024, 1), id_o, k > 0);
-        umma_commit(&sm.ofull[buf]);
-        umma_commit(&sm.empty[slot]);
-        umma_commit(&sm.pempty[i % NP]);
-        ++it;
-        return true;
-      };
       const int n = st.left;
-      if (n > 0) {
-        ok = scores(0);
-        w.next(p);
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        if (i + 1 < n) {
-          ok = scores(i + 1);
+      bool ok = true;
+      for (int i = 0; i < n + kAhead; ++i) {
+        if (i < n) {  // scores of tile i
+          const int slot = it % SLOTS, buf = i % NS;
+          if (w.first(st)) {
+            ok = wait_for(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
+            if (!ok) break;
+            ++items;
+          }
+          ok = wait_for(&sm.full[slot], (it / SLOTS) & 1, abort_flag) &&
+               wait_for(&sm.sempty[buf], ((i / NS) & 1) ^ 1, abort_flag);
           if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = smem_desc<RB>(s0 + slot * C::SLOT, D * 8, 1);
+          const uint64_t b = smem_desc<RB>(q0 + ((items - 1) % NQ) * C::QBYTES, RB * 8, 1);
+#pragma unroll 1
+          for (int ch = 0; ch < C::CH; ++ch)
+#pragma unroll
+            for (int x = 0; x < RB / 32; ++x)  // addresses in 16-byte units
+              umma_f8(tmem + C::S_COL + buf * N2, a + ch * (8 * RB / 16) + 2 * x,
+                      b + ch * (N2 * RB / 16) + 2 * x, id_s, ch + x > 0);
+          umma_commit(&sm.sfull[buf]);
+          umma_commit(&sm.empty[slot]);
+          if (w.last()) umma_commit(&sm.qempty[(items - 1) % NQ]);
+          ++it;
           w.next(p);
         }
-        ok = outputs(i);
+        if (i >= kAhead) {  // output tile
+          const int o = i - kAhead, slot = it % SLOTS, buf = o % NO;
+          ok = wait_for(&sm.full[slot], (it / SLOTS) & 1, abort_flag) &&
+               wait_for(&sm.pfull[o % NP], (o / NP) & 1, abort_flag) &&
+               wait_for(&sm.oempty[buf], ((o / NO) & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = smem_desc<RB>(s0 + slot * C::SLOT, D * 8, 0);
+          const uint64_t b = smem_desc<128>(pb0 + (o % NP) * C::PBYTES, 1024, 1);
+#pragma unroll 1
+          for (int c = 0; c < MT; ++c)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              umma_f8(tmem + C::O_COL + (buf * MT + c) * N2, a + c * (8 * RB / 16) + k * (2 * D),
+                      b + 2 * k, id_o, k > 0);
+          umma_commit(&sm.ofull[buf]);
+          umma_commit(&sm.empty[slot]);
+          umma_commit(&sm.pempty[o % NP]);
+          ++it;
+        }
       }
       if (!ok) fail();
       umma_commit(&sm.drain);
@@ -509,61 +573,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp < 4) {
     // -------------------------------------------------------------------- query splitter
-    // Rows in turn over the two warps: scale to at most 256, split, store swizzled.
-    Walk w;
-    w.begin(p, st);
+    // Rows in turn over the two warps, four at a time: scale to at most 256, split, store
+    // swizzled.
     uint32_t items = 0;
     const int half = warp - 2;
+    constexpr int E = D / 64;  // pairs a lane holds of a row: elements 2 lane + 64 e
     while (w.left > 0) {
       const int qb = items % NQ;
-      const bool free = mbar_wait(&sm.qempty[qb], ((items / NQ) & 1) ^ 1, abort_flag);
-      if (!__all_sync(0xffffffffu, free)) {
-        if (lane == 0) fail();
-        break;
-      }
       uint8_t *dst = qbuf + qb * C::QBYTES;
-      constexpr int E = D / 32;  // elements a lane holds of a row: pairs at 2 lane + 64 e
-#pragma unroll 2
-      for (int r = half; r < NR; r += 2) {
-        const int row = row0 + r;
-        float x[E];
-        float m = 0.f;
-        if (r < p.RG && row < p.M) {
+#pragma unroll 1
+      for (int r0 = half; r0 < NR; r0 += 8) {
+        uint32_t x[4][E];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = r0 + 2 * u, row = row0 + r;
           const int j = row / p.G, h = w.g * p.G + row % p.G;
           const uint32_t *src = reinterpret_cast<const uint32_t *>(
               p.q + (((size_t)w.b * p.n_q + j) * p.Hq + h) * D);
 #pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const uint32_t v = src[lane + 32 * e];
-            x[2 * e] = __uint_as_float(v << 16);
-            x[2 * e + 1] = __uint_as_float(v & 0xffff0000u);
+          for (int e = 0; e < E; ++e) x[u][e] = r < rows ? src[lane + 32 * e] : 0u;
+        }
+        if (r0 == half) {  // the loads are on their way
+          const bool free = wait_for(&sm.qempty[qb], ((items / NQ) & 1) ^ 1, abort_flag);
+          if (!__all_sync(0xffffffffu, free)) {
+            if (lane == 0) fail();
+            goto splitter_done;
           }
+        }
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u) {
+          const int r = r0 + 2 * u;
+          float m = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
-            const float a = fabsf(x[e]);
-            if (a < INFINITY) m = fmaxf(m, a);
-            else x[e] = __int_as_float(0x7fc00000);  // the row's output is NaN
+            const float a = fabsf(__uint_as_float(x[0][e] << 16));
+            const float b = fabsf(__uint_as_float(x[0][e] & 0xffff0000u));
+            m = fmaxf(m, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
           }
-        } else {
+          m = redux_max(m);
+          // 2^ex with m <= 256 * 2^ex, ex >= -100
+          const int ex = max((int)(__float_as_uint(m) >> 23) - 127 + 1 - 8, -100);
+          const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+          if (lane == 0) sm.qs[qb][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
-          for (int e = 0; e < E; ++e) x[e] = 0.f;
-        }
-        m = redux_max(m);
-        // 2^e with m <= 256 * 2^e, e >= -100
-        const int ex = max((int)(__float_as_uint(m) >> 23) - 127 + 1 - 8, -100);
-        const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-        if (lane == 0) sm.qs[qb][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+          for (int e = 0; e < E; ++e) {
+            float a = __uint_as_float(x[0][e] << 16), b = __uint_as_float(x[0][e] & 0xffff0000u);
+            // an infinity becomes NaN, and with it the row's output
+            if (!(fabsf(a) < INFINITY)) a = __int_as_float(0x7fc00000);
+            if (!(fabsf(b) < INFINITY)) b = __int_as_float(0x7fc00000);
+            uint32_t hi, lo;
+            split2(a * inv, b * inv, hi, lo);
+            const int col = 2 * lane + 64 * e;
+            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, r, col)) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, NR + r, col)) = (uint16_t)lo;
+          }
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) {
-          uint32_t hi, lo;
-          split2(x[2 * e] * inv, x[2 * e + 1] * inv, hi, lo);
-          const int col = 2 * lane + 64 * e;
-          *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, r, col)) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, NR + r, col)) = (uint16_t)lo;
+          for (int v = 0; v < 3; ++v)
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[v][e] = x[v + 1][e];
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm.qfull[qb]);
+      warp_arrive(&sm.qfull[qb]);
       ++items;
       do {  // to the next item
         const bool end = w.last();
@@ -571,258 +642,254 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (end) break;
       } while (true);
     }
-  } else if (warp < 8) {
+  splitter_done:;
+  } else if (warp < 4 + 4 * SG) {
     // -------------------------------------------------------------------- softmax
-    const int wq = warp - 4, key = wq * 32 + lane;
+    // Thread = key, eight rows of the warpgroup.
+    const int wg = (warp - 4) >> 2, wq = warp & 3, key = wq * 32 + lane, wr = warp - 4;
+    const int r0 = 8 * wg;
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-    Walk w;
-    w.begin(p, st);
     bool bad = false;
-    float m_run = -INFINITY;  // of row `lane`
-    float l[NR];
-    float qsc[NR];
+    float m_run = -INFINITY;  // of row r0 + lane
+    float l[8], qsc[8];
     uint32_t items = 0;
+    const int j_first = sm.rowj[0], j_last = sm.rowj[NR - 1];
     for (int i = 0; w.left > 0; ++i, w.next(p)) {
-      const int buf = i & 1;
-      const int pos = w.pos() + key;
+      const int buf = i % NS;
+      const int p0 = w.pos(), pos = p0 + key;
       if (w.first(st)) {
         // the splitter wrote the rows' scales before the scores were computed
-        bad |= !mbar_wait(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
+        bad |= !wait_for(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
         ++items;
         m_run = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < 8; ++r) {
           l[r] = 0.f;
-          qsc[r] = sm.qs[(items - 1) % NQ][r] * p.scale_log2;
+          qsc[r] = sm.qs[(items - 1) % NQ][r0 + r] * p.scale_log2;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.qempty[(items - 1) % NQ]);
+        warp_arrive(&sm.qempty[(items - 1) % NQ]);
       }
       const int ring = i % kScaleRing;
-      bad |= !mbar_wait(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
+      bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
       const float ks = sm.scales[ring][0][key >> 4];
       const float vs = fmaxf(sm.scales[ring][1][key >> 4], 0x1p-100f);
-      mbar_arrive(&sm.sc_empty[ring]);
-      const bool inside = pos >= w.s.lo && pos <= w.s.hi && ks >= 0.f;
-      bad |= !mbar_wait(&sm.sfull[buf], (i >> 1) & 1, abort_flag);
+      const bool hole = sm.hole[ring] != 0;
+      warp_arrive(&sm.sc_empty[ring]);
+      const float lvs = log2f(vs), rvs = 1.f / vs;
+      // a tile at a range's end, where not every row attends to every key
+      const bool edge = hole || p0 < row_lo(p, w.s, j_last) ||
+                        p0 + kTile - 1 > row_hi(p, w.s, j_first);
+      bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
       tc_fence_after();
-      float t[NR];
+      float t[8];
       {
-        uint32_t v[N2];
-#pragma unroll
-        for (int c = 0; c < N2; c += 16) {
-          uint32_t(&x)[16] = *reinterpret_cast<uint32_t(*)[16]>(&v[c]);
-          tmem_ld16(tmem + C::S_COL + buf * N2 + c + lane_base, x);
-        }
+        uint32_t hi[8], lo[8];
+        tmem_ld8(tmem + C::S_COL + buf * N2 + r0 + lane_base, hi);
+        tmem_ld8(tmem + C::S_COL + buf * N2 + NR + r0 + lane_base, lo);
         tmem_ld_wait();
         tc_fence_before();
-        mbar_arrive(&sm.sempty[buf]);
-        const float lvs = log2f(vs);
+        warp_arrive(&sm.sempty[buf]);
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const float s = fmaf(__uint_as_float(v[NR + r]), 0.0625f, __uint_as_float(v[r]));
+        for (int r = 0; r < 8; ++r) {
+          const float s = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
           t[r] = fmaf(s * ks, qsc[r], lvs);
         }
       }
-      // keys of a tile at a range's end that not every row attends to
-      const int last_row = min(row0 + p.RG, p.M) - 1;
-      const bool edge = w.pos() < row_lo(p, w.s, last_row) ||
-                        w.pos() + kTile - 1 > row_hi(p, w.s, row0) ||
-                        __any_sync(0xffffffffu, !inside);
-      bool some = false;  // masked for a row of the group
+      bool nan_v = false;
       if (edge) {
+        const bool inside = pos >= w.s.lo && pos <= w.s.hi && ks >= 0.f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-          const int row = min(row0 + r, last_row);
-          if (!inside || pos < row_lo(p, w.s, row) || pos > row_hi(p, w.s, row)) {
-            t[r] = -INFINITY;
-            some = true;
-          }
+        for (int r = 0; r < 8; ++r) {
+          const int j = sm.rowj[r0 + r];
+          if (!inside || pos < row_lo(p, w.s, j) || pos > row_hi(p, w.s, j)) t[r] = -INFINITY;
         }
+        // V rows that no query attends to may hold any codes, and 0 * NaN is NaN: they are
+        // cleared; a NaN that only some queries attend to is cleared and goes into their l
+        const bool part =
+            inside && (pos < row_lo(p, w.s, j_last) || pos > row_hi(p, w.s, j_first));
+        const uint32_t vit = min(i + kAhead + 1, st.left) + i;  // V_i in the ring's order
+        bad |= !wait_for(&sm.full[vit % SLOTS], (vit / SLOTS) & 1, abort_flag);
+        uint8_t *v = slots + (size_t)(vit % SLOTS) * C::SLOT + (key >> 3) * (8 * D) + (key & 7) * RB;
+        // bytes 0x7f and 0xff: bit 7 of each such byte
+        auto nan = [](uint32_t z) { return ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+        if (part)
+#pragma unroll 1
+          for (int u = 0; u < D; u += 16) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(v + u / RB * (8 * RB) +
+                                                             ((u + 16 * lane) & (RB - 1)));
+            nan_v |= (nan(y.x) | nan(y.y) | nan(y.z) | nan(y.w)) != 0;
+          }
+        // every warpgroup has seen the codes before the first one clears them
+        bad = barrier_or(1, 128 * SG, bad);
+        if (wg == 0 && !bad && (!inside || (part && nan_v)))
+#pragma unroll 1
+          for (int u = 0; u < D; u += 16) {
+            uint4 *x = reinterpret_cast<uint4 *>(v + u / RB * (8 * RB) +
+                                                 ((u + 16 * lane) & (RB - 1)));
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (inside) {
+              auto clear = [&](uint32_t z) { return z & ~((nan(z) >> 7) * 0xffu); };
+              y = *x;
+              y = make_uint4(clear(y.x), clear(y.y), clear(y.z), clear(y.w));
+            }
+            *x = y;
+          }
       }
       // maxima of the tile: lane r ends up with row r's
       {
         float mx = -INFINITY;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < 8; ++r) {
           const float v = redux_max(t[r]);
           if (lane == r) mx = v;
         }
-        if (lane < NR) sm.red[buf][wq][lane] = mx;
+        if (lane < 8) sm.red[wg][i & 1][wq][lane] = mx;
       }
-      bad = softmax_barrier(bad);
+      bad = barrier_or(2 + wg, 128, bad);
       if (bad) break;
-      if (lane < NR) {
-        float tm = sm.red[buf][0][lane];
+      if (lane < 8) {
+        float tm = sm.red[wg][i & 1][0][lane];
 #pragma unroll
-        for (int q = 1; q < 4; ++q) tm = fmaxf(tm, sm.red[buf][q][lane]);
+        for (int q = 1; q < 4; ++q) tm = fmaxf(tm, sm.red[wg][i & 1][q][lane]);
         if (tm != tm) tm = 0.f;  // nothing but NaN: the weights are, and l and O become NaN
         const float m_new = fmaxf(m_run, tm);
         const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
         const float beta = tm == -INFINITY ? 0.f : ex2_approx(tm - m_new) * 0x1p-8f;
         m_run = m_new;
-        sm.row[wq][0][lane] = tm == -INFINITY ? 0.f : tm - 8.f;
-        sm.row[wq][1][lane] = alpha;
-        sm.row[wq][2][lane] = beta;
+        sm.row[wr][0][lane] = tm == -INFINITY ? 0.f : tm - 8.f;
+        sm.row[wr][1][lane] = alpha;
+        sm.row[wr][2][lane] = beta;
       }
       __syncwarp();
-      bad |= !mbar_wait(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
+      bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
       if (wq == 0) {
-        // tile i - 4's pair is read: this buffer's last product waited for tile i - 4's output
-        // to be read
-        if (lane < NR) sm.ab[i & 3][lane] = make_float2(sm.row[0][1][lane], sm.row[0][2][lane]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.abfull[i & 3]);
+        // tile i - 4's pair is read: tile i - 2's output product, which this thread has seen
+        // finish, waited for tile i - 4's output to be read
+        if (lane < 8)
+          sm.ab[i & 3][r0 + lane] = make_float2(sm.row[wr][1][lane], sm.row[wr][2][lane]);
+        warp_arrive(&sm.abfull[i & 3]);
       }
-      bool nan_v = false;
-      if (__any_sync(0xffffffffu, some)) {
-        // V rows that no query attends to may hold any codes, and 0 * NaN is NaN: they are
-        // cleared; a NaN that only some queries attend to is cleared and goes into their l
-        const uint32_t vit = 2 * i + (i + 1 < st.left ? 2 : 1);  // V_i in the ring's order
-        bad |= !mbar_wait(&sm.full[vit % SLOTS], (vit / SLOTS) & 1, abort_flag);
-        if (some && !bad) {
-          uint8_t *v = slots + (size_t)(vit % SLOTS) * C::SLOT + (key >> 3) * (8 * D) +
-                       (key & 7) * RB;
-          for (int c = 0; c < C::CH; ++c)
-            for (int u = 0; u < RB; u += 16) {
-              uint4 *x = reinterpret_cast<uint4 *>(v + c * 8 * RB + u);
-              if (!inside) {
-                *x = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 y = *x;
-                // bytes 0x7f / 0xff: 0x80 in each such byte of m
-                auto nan = [](uint32_t z) { return ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
-                const uint32_t a = nan(y.x), b = nan(y.y), c2 = nan(y.z), d = nan(y.w);
-                if (a | b | c2 | d) {
-                  nan_v = true;
-                  auto clear = [](uint32_t z, uint32_t n) { return z & ~((n >> 7) * 0xffu); };
-                  *x = make_uint4(clear(y.x, a), clear(y.y, b), clear(y.z, c2), clear(y.w, d));
-                }
-              }
-            }
-        }
-      }
-      const float rvs = 1.f / vs;
       uint8_t *pd = pbuf + (i % NP) * C::PBYTES;
 #pragma unroll
-      for (int r = 0; r < NR; r += 2) {
-        const float *mx = &sm.row[wq][0][r], *al = &sm.row[wq][1][r], *be = &sm.row[wq][2][r];
-        const float w0 = ex2_approx(t[r] - mx[0]), w1 = ex2_approx(t[r + 1] - mx[1]);
+      for (int r = 0; r < 8; r += 2) {
+        const float2 mx = *reinterpret_cast<const float2 *>(&sm.row[wr][0][r]);
+        const float2 al = *reinterpret_cast<const float2 *>(&sm.row[wr][1][r]);
+        const float2 be = *reinterpret_cast<const float2 *>(&sm.row[wr][2][r]);
+        const float w0 = ex2_approx(t[r] - mx.x), w1 = ex2_approx(t[r + 1] - mx.y);
         float f0 = rvs, f1 = rvs;
         if (nan_v) {
           if (t[r] != -INFINITY) f0 = __int_as_float(0x7fc00000);
           if (t[r + 1] != -INFINITY) f1 = __int_as_float(0x7fc00000);
         }
-        l[r] = fmaf(l[r], al[0], w0 * f0 * be[0]);
-        l[r + 1] = fmaf(l[r + 1], al[1], w1 * f1 * be[1]);
+        l[r] = fmaf(l[r], al.x, w0 * f0 * be.x);
+        l[r + 1] = fmaf(l[r + 1], al.y, w1 * f1 * be.y);
         uint32_t hi, lo;
         split2(w0, w1, hi, lo);
-        pd[tile_byte<128>(N2, r, key)] = (uint8_t)hi;
-        pd[tile_byte<128>(N2, r + 1, key)] = (uint8_t)(hi >> 8);
-        pd[tile_byte<128>(N2, NR + r, key)] = (uint8_t)lo;
-        pd[tile_byte<128>(N2, NR + r + 1, key)] = (uint8_t)(lo >> 8);
+        pd[tile_byte<128>(N2, r0 + r, key)] = (uint8_t)hi;
+        pd[tile_byte<128>(N2, r0 + r + 1, key)] = (uint8_t)(hi >> 8);
+        pd[tile_byte<128>(N2, NR + r0 + r, key)] = (uint8_t)lo;
+        pd[tile_byte<128>(N2, NR + r0 + r + 1, key)] = (uint8_t)(lo >> 8);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&sm.pfull[i % NP]);
-      __syncwarp();
+      warp_arrive(&sm.pfull[i % NP]);
       if (w.last()) {
-        // l over the 128 keys; lane r of warp 0 hands (m, l) of row r over
+        // l over the 128 keys; lane r of the warpgroup's first warp hands (m, l) of row r over
         const int lb = (items - 1) & 1;
-        bad |= !mbar_wait(&sm.lempty[lb], (((items - 1) >> 1) & 1) ^ 1, abort_flag);
+        bad |= !wait_for(&sm.lempty[lb], (((items - 1) >> 1) & 1) ^ 1, abort_flag);
         float mine = 0.f;
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
+        for (int r = 0; r < 8; ++r) {
           float v = l[r];
           for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
           if (lane == r) mine = v;
         }
-        if (lane < NR) sm.red[buf ^ 1][wq][lane] = mine;
-        bad = softmax_barrier(bad);
+        float (&red)[4][8] = sm.red[wg][(i & 1) ^ 1];
+        if (lane < 8) red[wq][lane] = mine;
+        bad = barrier_or(2 + wg, 128, bad);
         if (bad) break;
-        if (wq == 0 && lane < NR) {
-          const float *x = &sm.red[buf ^ 1][0][lane];
-          sm.ml[lb][lane] = make_float2(m_run, x[0] + x[NR] + x[2 * NR] + x[3 * NR]);
-        }
-        // the next tile writes red[buf ^ 1] again: not before warp 0 has read it
-        bad = softmax_barrier(bad);
-        mbar_arrive(&sm.lfull[lb]);
+        if (wq == 0 && lane < 8)
+          sm.ml[lb][r0 + lane] =
+              make_float2(m_run, red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]);
+        // the next tile writes there again: not before the first warp has read it
+        bad = barrier_or(2 + wg, 128, bad);
+        warp_arrive(&sm.lfull[lb]);
         if (bad) break;
       }
     }
     if (bad && lane == 0) fail();
   } else {
     // -------------------------------------------------------------------- joining warps
-    const int wq = warp - 8, col = wq * 32 + lane;
+    const int jg = (warp - 4 - 4 * SG) >> 2, wq = warp & 3, col = wq * 32 + lane;
+    const int c0 = jg * MJ;  // first chunk of the warpgroup
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-    Walk w;
-    w.begin(p, st);
     bool ok = true;
-    float acc[MT][NR];
+    float acc[MJ][NR];
     uint32_t items = 0;
     bool whole = false;
     for (int i = 0; w.left > 0; ++i, w.next(p)) {
-      const int buf = i & 1;
+      const int buf = i % NO;
       if (w.first(st)) {
         whole = w.tau == 0 && w.left >= w.s.n;
         ++items;
 #pragma unroll
-        for (int c = 0; c < MT; ++c)
+        for (int c = 0; c < MJ; ++c)
 #pragma unroll
           for (int r = 0; r < NR; ++r) acc[c][r] = 0.f;
       }
-      ok = mbar_wait(&sm.abfull[i & 3], (i >> 2) & 1, abort_flag) &&
-           mbar_wait(&sm.ofull[buf], (i >> 1) & 1, abort_flag);
+      ok = wait_for(&sm.abfull[i & 3], (i >> 2) & 1, abort_flag) &&
+           wait_for(&sm.ofull[buf], (i / NO) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       if (D >= 128 || wq < 2) {
+        const uint32_t o0 = tmem + C::O_COL + (buf * MT + c0) * N2 + lane_base;
 #pragma unroll
-        for (int c = 0; c < MT; ++c) {
-          uint32_t v[N2];
+        for (int c = 0; c < MJ; ++c)
 #pragma unroll
-          for (int k = 0; k < N2; k += 16) {
-            uint32_t(&x)[16] = *reinterpret_cast<uint32_t(*)[16]>(&v[k]);
-            tmem_ld16(tmem + C::O_COL + (buf * MT + c) * N2 + k + lane_base, x);
+          for (int r = 0; r < NR; r += 8) {
+            uint32_t hi[8], lo[8];
+            tmem_ld8(o0 + c * N2 + r, hi);
+            tmem_ld8(o0 + c * N2 + NR + r, lo);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float2 ab = sm.ab[i & 3][r + e];
+              const float o = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e]));
+              acc[c][r + e] = fmaf(acc[c][r + e], ab.x, o * ab.y);
+            }
           }
-          tmem_ld_wait();
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float2 ab = sm.ab[i & 3][r];
-            const float o = fmaf(__uint_as_float(v[NR + r]), 0.0625f, __uint_as_float(v[r]));
-            acc[c][r] = fmaf(acc[c][r], ab.x, o * ab.y);
-          }
-        }
       }
       tc_fence_before();
-      mbar_arrive(&sm.oempty[buf]);
+      warp_arrive(&sm.oempty[buf]);
       if (!w.last()) continue;
       const int lb = (items - 1) & 1;
-      ok = mbar_wait(&sm.lfull[lb], ((items - 1) >> 1) & 1, abort_flag);
+      ok = wait_for(&sm.lfull[lb], ((items - 1) >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int rows = min(p.RG, p.M - row0);
       const size_t item = (size_t)w.b * p.Hkv + w.g;
+      if (D >= 128 || wq < 2) {
 #pragma unroll
-      for (int r = 0; r < NR; ++r) {
-        if (r >= rows) continue;
-        const float2 ml = sm.ml[lb][r];
-        const int row = row0 + r;
-        if (whole) {
-          const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;  // no key: a zero row
-          __nv_bfloat16 *dst =
-              p.out + (((size_t)w.b * p.n_q + row / p.G) * p.Hq + w.g * p.G + row % p.G) * D;
+        for (int r = 0; r < NR; ++r) {
+          if (r >= rows) continue;
+          const float2 ml = sm.ml[lb][r];
+          const int row = row0 + r, j = sm.rowj[r];
+          if (whole) {
+            const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;  // no key: a zero row
+            __nv_bfloat16 *dst =
+                p.out + (((size_t)w.b * p.n_q + j) * p.Hq + w.g * p.G + row - j * p.G) * D;
 #pragma unroll
-          for (int c = 0; c < MT; ++c)
-            if (D >= 128 || wq < 2) dst[c * 128 + col] = __float2bfloat16_rn(acc[c][r] * inv);
-        } else {
-          const size_t at = (item + cta) * (size_t)(p.R * p.RG) + row;
+            for (int c = 0; c < MJ; ++c)
+              dst[(c0 + c) * 128 + col] = __float2bfloat16_rn(acc[c][r] * inv);
+          } else {
+            const size_t at = (item + cta) * (size_t)(p.R * p.RG) + row;
 #pragma unroll
-          for (int c = 0; c < MT; ++c)
-            if (D >= 128 || wq < 2) p.ws_o[at * D + c * 128 + col] = acc[c][r];
-          if (wq == 0 && lane == 0) *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = ml;
+            for (int c = 0; c < MJ; ++c) p.ws_o[at * D + (c0 + c) * 128 + col] = acc[c][r];
+            if (jg == 0 && wq == 0 && lane == 0)
+              *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = ml;
+          }
         }
       }
-      mbar_arrive(&sm.lempty[lb]);
+      warp_arrive(&sm.lempty[lb]);
     }
     if (!ok && lane == 0) fail();
   }
@@ -838,24 +905,22 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
   pdl_wait();
   const int item = blockIdx.x, row = blockIdx.y;
   const int b = item / p.Hkv, g = item % p.Hkv;
-  __shared__ long long s_pre, s_total;
+  __shared__ unsigned s_pre, s_total;
   if (threadIdx.x < 32) {
-    long long pre = 0, total = 0;
+    unsigned pre = 0, total = 0;
     for (int i = threadIdx.x; i < p.B; i += 32) {
-      const long long n = (long long)seq_of(p, i, false).n * p.Hkv;
+      const unsigned n = seq_of(p, i, false).n * p.Hkv;
       total += n;
       if (i < b) pre += n;
     }
-    for (int o = 16; o > 0; o >>= 1) {
-      pre += __shfl_xor_sync(0xffffffffu, pre, o);
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
+    pre = __reduce_add_sync(0xffffffffu, pre);
+    total = __reduce_add_sync(0xffffffffu, total);
     if (threadIdx.x == 0) {
       s_pre = pre;
       s_total = total;
     }
   }
-  const int n = seq_of(p, b, false).n;
+  const unsigned n = seq_of(p, b, false).n;
   __syncthreads();
   __nv_bfloat16 *dst =
       p.out + (((size_t)b * p.n_q + row / p.G) * p.Hq + g * p.G + row % p.G) * p.D;
@@ -864,9 +929,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
     if (d < p.D) *reinterpret_cast<uint2 *>(dst + d) = make_uint2(0, 0);
     return;
   }
-  const long long total = s_total, first = s_pre + (long long)g * n, last = first + n - 1;
-  // CTA c holds tiles [total c / P, total (c + 1) / P)
-  const int c0 = (int)(((first + 1) * p.P - 1) / total), c1 = (int)(((last + 1) * p.P - 1) / total);
+  const unsigned total = s_total, P = min((unsigned)p.P, total), first = s_pre + g * n;
+  const int c0 = (int)share_of(total, first, P), c1 = (int)share_of(total, first + n - 1, P);
   if (c0 == c1) return;  // written by its only CTA
   const size_t pitch = (size_t)p.R * p.RG;
   float m = -INFINITY, den = 0.f;
@@ -878,8 +942,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int x = c + u;
-      // with fewer tiles than CTAs some hold none and wrote nothing
-      const bool held = x <= c1 && total * (x + 1) / p.P > total * x / p.P;
+      const bool held = x <= c1;
       const size_t at = ((size_t)item + x) * pitch + row;
       ml[u] = held ? *reinterpret_cast<const float2 *>(p.ws_ml + at * 2)
                    : make_float2(-INFINITY, 0.f);
@@ -938,7 +1001,7 @@ static sd_status launch_one(const CUtensorMap &km, const CUtensorMap &vm, const 
       return SD_ERR_CUDA;
     if (dev < 64) ready[dev] = 1;
   }
-  return cuda_status(launch(attn_q8_kernel<D, NR>, dim3(p.P * p.R), dim3(kThreads), C::SMEM, st,
+  return cuda_status(launch(attn_q8_kernel<D, NR>, dim3(p.P * p.R), dim3(C::THREADS), C::SMEM, st,
                             km, vm, p));
 }
 

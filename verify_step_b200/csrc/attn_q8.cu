@@ -26,6 +26,7 @@
 // output tile while tile i + 1 is.  The flattened (sequence, kv head, tile) list is split evenly
 // over the CTAs; shared items leave (o, m, l) partials that a second kernel joins in CTA order.
 #include <algorithm>
+#include <climits>
 
 #include "common.cuh"
 #include "host.cuh"
@@ -34,15 +35,17 @@ namespace sdv {
 namespace q8 {
 
 constexpr int kTile = 128;  // keys
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 8;
 // Score tiles computed ahead of the output products: V of a tile is then loaded when its weights
 // are nearly done, so it does not hold a ring slot through the softmax.
 constexpr int kAhead = 2;
+constexpr float kNone = -1e30f;  // maximum of no scores
 
 struct Params {
   int B, n_q, Hq, Hkv, G, D, bs, mbps, num_blocks, window, M;
   int is_draft, q_offset;
   int bk, box_bytes;  // keys and bytes of one TMA box
+  int row_groups;     // 8-row groups of a cache
   int R, RG;          // row groups of an item, rows of a group
   int P;              // CTAs of one row group
   float scale_log2;
@@ -123,15 +126,65 @@ struct Walk {
   }
   __device__ __forceinline__ bool last() const { return left == 1 || tau == s.n - 1; }
   __device__ __forceinline__ int pos() const { return s.p0 + tau * kTile; }
-  __device__ __forceinline__ void next(const Params &p) {
-    --left;
-    if (++tau < s.n || left == 0) return;
+  __device__ __forceinline__ void next(const Params &p) { advance(p, 1); }
+  // k tiles on, at most to the end of the item
+  __device__ __forceinline__ void advance(const Params &p, int k) {
+    left -= k;
+    tau += k;
+    if (tau < s.n || left == 0) return;
     tau = 0;
     if (++g < p.Hkv) return;
     g = 0;
     do {
       s = seq_of(p, ++b, false);
     } while (s.n == 0);  // left > 0: a later sequence has tiles
+  }
+};
+
+// The TMA boxes of a CTA's tiles, looked up a span of 32 boxes (of one item) at a time and one span
+// ahead: with a lookup per tile the table's latency and the index arithmetic took 1.9 us a tile.
+// Lane l holds box l: its row in the cache seen as a matrix of rows, -1 behind the last key, -2 where
+// the table names no block.  Such boxes are loaded from behind the tensor's end, which fills them
+// with zeros: their keys are masked, and 0 * V stays 0 whatever the slot held before.
+struct Boxes {
+  Walk w;
+  int row, n, k;  // tiles of the span, and the current one
+  int blk2, off2, g2, n2;  // the next span: block (the load is only waited for when the span
+                           // comes up), row in it (-1: none), kv head
+  int lb;         // log2 of a tile's boxes
+  __device__ __forceinline__ int boxes() const { return 1 << lb; }
+  __device__ __forceinline__ int box(int lane) const { return lane & (boxes() - 1); }
+  __device__ __forceinline__ bool turn(int lane) const { return lane >> lb == k; }
+  __device__ __forceinline__ void fetch(const Params &p, int lane) {
+    n2 = 0;
+    if (w.left == 0) return;
+    n2 = min(min(32 >> lb, w.s.n - w.tau), w.left);
+    const int pk = w.pos() + lane * p.bk;
+    off2 = -1;
+    g2 = w.g;
+    if (lane < n2 << lb && pk <= w.s.hi) {
+      const int bi = pk / p.bs;
+      off2 = pk - bi * p.bs;
+      blk2 = __ldg(p.table + (size_t)w.b * p.mbps + bi);
+    }
+    w.advance(p, n2);
+  }
+  __device__ __forceinline__ void begin(const Params &p, const Walk &at) {
+    w = at;
+    lb = 31 - __clz(kTile / p.bk);
+    n = k = n2 = 0;
+    off2 = -1;
+  }
+  // To the next tile; there is one.
+  __device__ __forceinline__ void next(const Params &p, int lane) {
+    if (++k < n) return;
+    do {  // twice at the beginning
+      row = off2 < 0 ? -1
+            : blk2 >= 0 && blk2 < p.num_blocks ? (blk2 * p.Hkv + g2) * p.bs + off2 : -2;
+      n = n2;
+      k = 0;
+      fetch(p, lane);
+    } while (n == 0);
   }
 };
 
@@ -147,7 +200,11 @@ struct Cfg {
   static constexpr int SG = NR / 8;
   static constexpr int MJ = MT * NR <= 48 ? MT : MT / 2 * NR <= 48 ? MT / 2 : 1;
   static constexpr int JG = MT / MJ;                  // joining warpgroups, MJ chunks each
-  static constexpr int THREADS = 128 * (1 + SG + JG);
+  // Softmax warpgroups in two sets that take the tiles in turn where one tile's chain of waits,
+  // exchange and rounding takes longer than the tile's bytes.
+  static constexpr int SETS = D < 512 && NR <= 8 ? 2 : 1;
+  static constexpr int SW = 4 * SG * SETS;            // softmax warps
+  static constexpr int THREADS = 32 * (4 + SW) + 128 * JG;
   static constexpr int SLOT = kTile * D;
   static constexpr int NQ = D == 512 ? 1 : 2;         // query buffers
   static constexpr int NP = D == 512 && NR == 24 ? 1 : 2;  // weight buffers
@@ -162,20 +219,20 @@ struct Cfg {
                                    : COLS <= 256 ? 256 : 512;
   static_assert(COLS <= 512, "tensor memory");
   struct Small {
-    float scales[kScaleRing][2][8];
-    float red[SG][2][4][8];
-    float row[4 * SG][3][8];  // per softmax warp: tile max - 8, alpha, beta
-    float2 ab[4][NR];         // alpha, beta for the joining warps
-    float2 ml[2][NR];         // m, l of an item
+    alignas(16) float scales[kScaleRing][2][8];  // K's and V's of each box of a tile; -1: no such box
+    alignas(16) float red[SETS * SG][2][4][8];
+    alignas(16) float tm[4][NR];          // tile maxima for the joining warps
+    alignas(16) float beta[4 * JG][NR];   // their factors of a tile, by warp
+    float2 ml[2][SETS][NR];   // frame and l of an item
     float qs[2][NR];          // 2^e scale of the query rows
-    int rowj[NR];             // query position of a row (row / G)
-    uint64_t full[8], empty[8];
-    uint64_t sc_full[kScaleRing], sc_empty[kScaleRing];
+    uint32_t nan_rows[2];     // of an item
+    alignas(16) int rowj[NR];             // query position of a row (row / G)
+    uint64_t kfull[8], vfull[8], empty[8];
+    uint64_t sc_full[kScaleRing];
     uint64_t qfull[2], qempty[2], sfull[NS], sempty[NS], pfull[2], pempty[2], ofull[2], oempty[2],
-        lfull[2], lempty[2], abfull[4], drain;
+        lfull[2], lempty[2], tmfull[4], drain[2];
     Start start;
     uint32_t tmem;
-    int hole[kScaleRing];     // a block of the tile does not exist
     int abort_flag;
   };
   static constexpr int FIXED = 1024 + NQ * QBYTES + NP * PBYTES + (int)sizeof(Small);
@@ -205,30 +262,45 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
                : "memory");
 }
 
-// D[tmem] (+)= A B^T, 8-bit floats, float32 accumulator.
+// D[tmem] (+)= A B^T, 8-bit floats, float32 accumulator.  The whole warp calls it and one elected lane
+// issues: with warp-uniform operands and control flow the descriptors stay in uniform registers
+// (issued from inside a one-lane branch a product took 70 ns to issue, more than to compute).
 __device__ __forceinline__ void umma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// umma_commit by the lane that issues for the warp.
+__device__ __forceinline__ void warp_commit(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
       : "memory");
 }
 
 // Shared-memory matrix descriptor: rows of RB = 128 or 64 bytes with the swizzle of that width,
 // 8-row groups sbo bytes apart.  K-major operands have one swizzled row per M/N index (the leading
 // offset is unused); MN-major ones one per K index, RB bytes of M, and lbo bytes to the next RB.
+// RB = 0, MN-major without swizzle: 16 bytes of M/N a K index, 8 K indexes in 128 bytes; the next 8
+// lbo, the next 16 of M/N sbo bytes further.
 template <int RB>
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t sbo, uint32_t lbo16) {
   return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)lbo16 << 16) |
          ((uint64_t)(sbo >> 4) << 32) | ((uint64_t)1 << 46) |
-         ((uint64_t)(RB == 128 ? 2 : 4) << 61);
+         ((uint64_t)(RB == 128 ? 2 : RB == 64 ? 4 : 0) << 61);
 }
 
-// kind::f8f6f4, e4m3 x e4m3 -> float32; a_mn: A is MN-major (bit 15).
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) |
+// kind::f8f6f4, e4m3 x e4m3 -> float32; a_mn, b_mn: the operand is MN-major (bits 15 and 16).
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
 
@@ -238,31 +310,61 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float2 e4m3x2_float(uint32_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)c));
-  float2 f;
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, "
-      "b;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
-}
-// x and y as hi + lo / 16, both parts e4m3 (two bytes each).
+// x and y (at most 448) as hi + lo / 16, both parts e4m3 (two bytes each).  What the high parts leave
+// is taken in f16: its 11 bits round x by 2^-12 of it, far below the low part's step.
 __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+  uint16_t l;
   hi = e4m3x2(x, y);
-  const float2 h = e4m3x2_float(hi);
-  lo = e4m3x2((x - h.x) * 16.f, (y - h.y) * 16.f);
+  asm("{\n\t.reg .b32 a, h;\n\t"
+      "cvt.rn.f16x2.f32 a, %3, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %1;\n\t"
+      "sub.f16x2 a, a, h;\n\t"
+      "mul.f16x2 a, a, %4;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, a;\n\t}"
+      : "=h"(l)
+      : "h"((uint16_t)hi), "f"(x), "f"(y), "r"(0x4c004c00u));  // 16, 16
+  lo = l;
 }
 
-// 32 lanes x 8 columns: thread i of the warp gets lane (base + i).
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
+// Maxima over the warp of eight values a lane: each step halves the rows a lane still holds, so
+// nine shuffles do for eight rows; lane l returns row l / 4.
+__device__ __forceinline__ float warp_max8(const float (&t)[8]) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool up = lane & 16;
+    a[k] = fmaxf(up ? t[4 + k] : t[k], __shfl_xor_sync(0xffffffffu, up ? t[k] : t[4 + k], 16));
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bool up = lane & 8;
+    b[k] = fmaxf(up ? a[2 + k] : a[k], __shfl_xor_sync(0xffffffffu, up ? a[k] : a[2 + k], 8));
+  }
+  const bool up = lane & 4;
+  float c = fmaxf(up ? b[1] : b[0], __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4));
+  c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 2));
+  return fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 1));
+}
+
+// Sums in the same way.
+__device__ __forceinline__ float warp_sum8(const float (&t)[8]) {
+  const int lane = threadIdx.x & 31;
+  float a[4], b[2];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const bool up = lane & 16;
+    a[k] = (up ? t[4 + k] : t[k]) + __shfl_xor_sync(0xffffffffu, up ? t[k] : t[4 + k], 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const bool up = lane & 8;
+    b[k] = (up ? a[2 + k] : a[k]) + __shfl_xor_sync(0xffffffffu, up ? a[k] : a[2 + k], 8);
+  }
+  const bool up = lane & 4;
+  float c = (up ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, up ? b[0] : b[1], 4);
+  c += __shfl_xor_sync(0xffffffffu, c, 2);
+  return c + __shfl_xor_sync(0xffffffffu, c, 1);
 }
 
 __device__ __forceinline__ float redux_max(float v) {
@@ -271,33 +373,47 @@ __device__ __forceinline__ float redux_max(float v) {
   return r;
 }
 
-// mbar_wait that sleeps in the hardware between tries: a spinning warp takes issue slots from the
-// warps that compute (B 8 verify at D 512: 157 us spinning).
-__device__ __forceinline__ bool try_wait_hint(uint64_t *bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
-}
+// mbar_wait with a short way through: a try suspends in the hardware for about 4 us, so a few thousand
+// of them in a loop of three instructions come before the abort flag and the 2 s limit are looked at.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
   unsigned long long t0 = 0;
-  while (!try_wait_hint(bar, parity)) {
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, 0;\n"
+        "TRY:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "add.u32 n, n, 1;\n\t"
+        "setp.lt.u32 q, n, 4096;\n\t"
+        "@q bra TRY;\n"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (__builtin_expect(ok, 1)) return true;
     const unsigned long long now = globaltimer_ns();
     if (t0 == 0) t0 = now;
     if (*abort || now - t0 > kWaitLimitNs) return false;
   }
-  return true;
 }
 
-// One arrival for the warp, once all its lanes are here (32 arrivals on one address serialise).
+// wait_for of a whole warp with one answer.  Every lane waits itself: a single polling lane saves
+// nothing and costs a divergent branch and a warp barrier per wait.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  return __all_sync(0xffffffffu, wait_for(bar, parity, abort));
+}
+
+// One arrival for the warp, once all its lanes are here (predicated, no branch).
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
 }
 
 // Barrier ``id`` of ``n`` threads that also tells whether any of them failed a wait.
@@ -322,16 +438,68 @@ __device__ __forceinline__ uint32_t tile_byte(int rows, int row, int col) {
   return (uint32_t)(chunk * rows * RB + row * RB + (((c >> 4) ^ x) << 4) + (c & 15));
 }
 
+// Whether some row of the group (queries j_first .. j_last) does not attend to some key of the tile.
+__device__ __forceinline__ bool is_edge(const Params &p, const Walk &w, int j_first, int j_last) {
+  return w.pos() < row_lo(p, w.s, j_last) || w.pos() + kTile - 1 > row_hi(p, w.s, j_first);
+}
+
+// V rows that no query attends to may hold any codes, and 0 * NaN is NaN: they are cleared.  A NaN that
+// only some queries attend to is cleared too, and the group's rows that see it are returned.  One
+// warp, a row (or the part of one that a lane's 16 bytes each cover) at a time.
+template <int D, int NR>
+__device__ __forceinline__ uint32_t clean_v(const Params &p, const Walk &w, uint8_t *tile,
+                                            const int *rowj, int lane) {
+  constexpr int RB = D >= 128 ? 128 : 64;
+  const int p0 = w.pos(), j_first = rowj[0], j_last = rowj[NR - 1];
+  uint32_t rows = 0;
+  // keys [0, before) and [after, end): not every row attends to them; behind end are zeros already
+  const int before = min(max(row_lo(p, w.s, j_last) - p0, 0), kTile);
+  const int after = max(row_hi(p, w.s, j_first) + 1 - p0, before);
+  const int end = min(w.s.p0 + ((w.s.hi - w.s.p0) / p.bk + 1) * p.bk - p0, kTile);
+#pragma unroll 1
+  for (int k = 0; k < before + max(end - after, 0); ++k) {
+    const int key = k < before ? k : after + k - before, pos = p0 + key;
+    const bool inside = pos >= w.s.lo && pos <= w.s.hi;
+    uint8_t *v = tile + (key >> 3) * (8 * D) + (key & 7) * RB;
+    bool any = false;
+    for (int u = 16 * lane; u < D; u += 512) {
+      uint4 *x = reinterpret_cast<uint4 *>(v + u / RB * (8 * RB) + u % RB);
+      if (!inside) {
+        *x = make_uint4(0, 0, 0, 0);
+      } else {
+        // bytes 0x7f and 0xff: bit 7 of each such byte
+        auto nan = [](uint32_t z) { return ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+        auto clear = [&](uint32_t z) { return z & ~((nan(z) >> 7) * 0xffu); };
+        const uint4 y = *x;
+        if (nan(y.x) | nan(y.y) | nan(y.z) | nan(y.w)) {
+          any = true;
+          *x = make_uint4(clear(y.x), clear(y.y), clear(y.z), clear(y.w));
+        }
+      }
+    }
+    if (__any_sync(0xffffffffu, any)) {
+      const int j = lane < NR ? rowj[lane] : 0;
+      rows |= __ballot_sync(0xffffffffu,
+                            lane < NR && pos >= row_lo(p, w.s, j) && pos <= row_hi(p, w.s, j));
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  return rows;
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     attn_q8_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
   using C = Cfg<D, NR>;
   constexpr int N2 = C::N2, MT = C::MT, RB = C::RB, SLOTS = C::SLOTS, NQ = C::NQ, NP = C::NP,
-                NO = C::NO, NS = C::NS, SG = C::SG, JG = C::JG, MJ = C::MJ;
+                NO = C::NO, NS = C::NS, SG = C::SG, SETS = C::SETS, MJ = C::MJ;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by pointer arithmetic, so that the compiler still knows it for shared memory (through an
+  // integer cast every access becomes a generic one with 64-bit addresses: B 64 at D 256, 252 us
+  // against 232)
+  uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t *slots = smem;
   uint8_t *qbuf = slots + (size_t)SLOTS * C::SLOT;
   uint8_t *pbuf = qbuf + NQ * C::QBYTES;
@@ -344,29 +512,28 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   const int rows = min(p.RG, p.M - row0);  // rows of this group
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&sm.full[i], 1);
+      mbar_init(&sm.kfull[i], 1);
+      mbar_init(&sm.vfull[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
-    for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&sm.sc_full[i], 16 + 1);
-      mbar_init(&sm.sc_empty[i], 4 * SG);
-    }
+    for (int i = 0; i < kScaleRing; ++i) mbar_init(&sm.sc_full[i], 8);
     for (int i = 0; i < NS; ++i) {
       mbar_init(&sm.sfull[i], 1);
       mbar_init(&sm.sempty[i], 4 * SG);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.qfull[i], 2);
-      mbar_init(&sm.qempty[i], 1 + 4 * SG);  // the item's last scores; its row scales are read
+      mbar_init(&sm.qfull[i], 1);
+      mbar_init(&sm.qempty[i], 1 + C::SW);  // the item's last scores; its row scales are read
       mbar_init(&sm.pfull[i], 4 * SG);
       mbar_init(&sm.pempty[i], 1);
       mbar_init(&sm.ofull[i], 1);
-      mbar_init(&sm.oempty[i], 4 * JG);
-      mbar_init(&sm.lfull[i], 4 * SG);
-      mbar_init(&sm.lempty[i], 4 * JG);
+      mbar_init(&sm.oempty[i], 4 * C::JG);
+      mbar_init(&sm.lfull[i], C::SW + 1);
+      mbar_init(&sm.lempty[i], 4 * C::JG);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sm.abfull[i], SG);
-    mbar_init(&sm.drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sm.tmfull[i], SG);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     sm.abort_flag = 0;
     fence_mbar_init();
   }
@@ -427,182 +594,192 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   Walk w;
   w.begin(p, st);
 
+  // The K and V tiles share one ring, in the order K0 .. K_ahead, V0, K, V1, ... in which the products
+  // need them: K_i is entry i, from the first V on 2 i - ahead, V_i entry min(i + ahead + 1, tiles) + i.
+  // One warp fills it in that order.  Two warps empty it, so each has its own barrier of a slot:
+  // a wait never starts more than one phase early, and the parity says which phase it is.
   if (warp == 0) {
-    // -------------------------------------------------------------------- TMA producer
-    // Ring order K0 .. K_ahead, V0, K, V1, ...: the order in which the products need the tiles.
+    // -------------------------------------------------------------------- TMA
     tma_prefetch_desc(&kmap);
     tma_prefetch_desc(&vmap);
     const uint64_t policy = l2_policy_evict_first();
-    uint32_t it = 0;
+    Boxes x;
+    x.begin(p, w);
+    int slot = 0;
+    uint32_t phase = 0, k_fills = 0, v_fills = 0;  // parities of each slot's fills
     bool ok = true;
-    const int boxes = kTile / p.bk, per_blk = p.bs / p.bk;
-    int v_row[kAhead + 1], v_boxes[kAhead + 1];  // boxes of the last tiles: lane i holds its i-th
-    auto load_slot = [&](const CUtensorMap *map, int row, uint32_t bytes) {
-      const int slot = it % SLOTS;
-      const bool free = wait_for(&sm.empty[slot], ((it / SLOTS) & 1) ^ 1, abort_flag);
-      if (!__all_sync(0xffffffffu, free)) {
-        if (lane == 0) fail();
-        return false;
+    int zs[kAhead + 1] = {};  // group coordinates of the last tiles' boxes, V's turn being later
+    bool turn[kAhead + 1] = {};
+    for (int i = 0; i < st.left + kAhead && ok; ++i) {
+#pragma unroll
+      for (int u = kAhead; u > 0; --u) {
+        zs[u] = zs[u - 1];
+        turn[u] = turn[u - 1];
       }
-      if (lane == 0) mbar_arrive_expect_tx(&sm.full[slot], bytes);
-      __syncwarp();
-      if (row >= 0)
-        tma_load_4d(slots + (size_t)slot * C::SLOT + lane * p.box_bytes, map, &sm.full[slot],
-                    row >> 3, policy);
-      ++it;
-      return true;
-    };
-    for (int i = 0; i < st.left + kAhead; ++i) {
-      int row = -1, nb = 0;
       if (i < st.left) {
-        const int pk = w.pos() + lane * p.bk;  // lane's box
-        bool hole = false;
-        if (lane < boxes && pk <= w.s.hi) {
-          const int blk = p.table[(size_t)w.b * p.mbps + pk / p.bs];
-          if (blk >= 0 && blk < p.num_blocks)
-            row = (blk * p.Hkv + w.g) * p.bs + (pk / p.bk % per_blk) * p.bk;
-          else
-            hole = true;
+        x.next(p, lane);
+        turn[0] = x.turn(lane);
+        zs[0] = x.row >= 0 ? x.row >> 3 : p.row_groups;
+      }
+#pragma unroll 1
+      for (int v = i < st.left ? 0 : 1; v <= (i >= kAhead ? 1 : 0); ++v) {
+        ok = warp_wait(&sm.empty[slot], phase ^ 1, abort_flag);
+        if (!ok) break;
+        uint64_t *full = v ? &sm.vfull[slot] : &sm.kfull[slot];
+        if (lane == 0) mbar_arrive_expect_tx(full, C::SLOT);
+        __syncwarp();
+        if (v ? turn[kAhead] : turn[0])
+          tma_load_4d(slots + (size_t)slot * C::SLOT + x.box(lane) * p.box_bytes, v ? &vmap : &kmap,
+                      full, v ? zs[kAhead] : zs[0], policy);
+        (v ? v_fills : k_fills) ^= 1u << slot;
+        if (++slot == SLOTS) {
+          slot = 0;
+          phase ^= 1;
         }
-        nb = __popc(__ballot_sync(0xffffffffu, row >= 0));
-        hole = __any_sync(0xffffffffu, hole);
-        const int r = i % kScaleRing;
-        ok = wait_for(&sm.sc_empty[r], ((i / kScaleRing) & 1) ^ 1, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) fail();
-          break;
-        }
-        if (lane == 0) {
-          if (hole) record_status(p.status, SD_ERR_DEVICE);
-          sm.hole[r] = hole;
-          mbar_arrive(&sm.sc_full[r]);
-        }
-        // scales of the 16-key group lane & 7
-        const int grp = lane & 7;
-        const int srow = __shfl_sync(0xffffffffu, row, grp * 16 / p.bk);
-        if (lane < 16) {
-          float *dst = &sm.scales[r][lane >> 3][grp];
-          if (srow >= 0) {
-            cp_async_4(dst, (lane < 8 ? p.ks : p.vs) + srow / p.bs);
-            cp_async_arrive(&sm.sc_full[r]);
-          } else {
-            *dst = -1.f;  // no such block: its keys are masked
-            mbar_arrive(&sm.sc_full[r]);
+        if (v == 0) {
+          // The tile's scales.  Their place is free: the slot's last entry was K_{i-4} or younger (or a
+          // V younger than that), whose scores needed the buffer of tile i - 7, read after its scales.
+          const int r = i % kScaleRing, box = x.box(lane);
+          if (turn[0]) {
+            if (x.row >= 0) {
+              const int at = x.row / p.bs;
+              cp_async_4(&sm.scales[r][0][box], p.ks + at);
+              cp_async_4(&sm.scales[r][1][box], p.vs + at);
+              cp_async_arrive(&sm.sc_full[r]);
+            } else {
+              sm.scales[r][0][box] = -1.f;  // its keys are masked
+              mbar_arrive(&sm.sc_full[r]);
+              if (x.row == -2) record_status(p.status, SD_ERR_DEVICE);
+            }
           }
+          if (lane < 8 - x.boxes()) mbar_arrive(&sm.sc_full[r]);
         }
-        ok = load_slot(&kmap, row, nb * p.box_bytes);
-        if (!ok) break;
-        w.next(p);
-      }
-#pragma unroll
-      for (int k = kAhead; k > 0; --k) {
-        v_row[k] = v_row[k - 1];
-        v_boxes[k] = v_boxes[k - 1];
-      }
-      v_row[0] = row;
-      v_boxes[0] = nb;
-      if (i >= kAhead) {
-        ok = load_slot(&vmap, v_row[kAhead], v_boxes[kAhead] * p.box_bytes);
-        if (!ok) break;
       }
     }
-    if (!ok && lane == 0)
-      for (uint32_t j = it > (uint32_t)SLOTS ? it - SLOTS : 0; j < it; ++j)
-        mbar_wait_timed(&sm.full[j % SLOTS], (j / SLOTS) & 1);
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 1) {
-    // -------------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_s = idesc_f8(128, N2, false), id_o = idesc_f8(128, N2, true);
-      const uint32_t s0 = smem_u32(slots), q0 = smem_u32(qbuf), pb0 = smem_u32(pbuf);
-      uint32_t it = 0, items = 0;
-      const int n = st.left;
-      bool ok = true;
-      for (int i = 0; i < n + kAhead; ++i) {
-        if (i < n) {  // scores of tile i
-          const int slot = it % SLOTS, buf = i % NS;
-          if (w.first(st)) {
-            ok = wait_for(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
-            if (!ok) break;
-            ++items;
-          }
-          ok = wait_for(&sm.full[slot], (it / SLOTS) & 1, abort_flag) &&
-               wait_for(&sm.sempty[buf], ((i / NS) & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = smem_desc<RB>(s0 + slot * C::SLOT, D * 8, 1);
-          const uint64_t b = smem_desc<RB>(q0 + ((items - 1) % NQ) * C::QBYTES, RB * 8, 1);
-#pragma unroll 1
-          for (int ch = 0; ch < C::CH; ++ch)
-#pragma unroll
-            for (int x = 0; x < RB / 32; ++x)  // addresses in 16-byte units
-              umma_f8(tmem + C::S_COL + buf * N2, a + ch * (8 * RB / 16) + 2 * x,
-                      b + ch * (N2 * RB / 16) + 2 * x, id_s, ch + x > 0);
-          umma_commit(&sm.sfull[buf]);
-          umma_commit(&sm.empty[slot]);
-          if (w.last()) umma_commit(&sm.qempty[(items - 1) % NQ]);
-          ++it;
-          w.next(p);
-        }
-        if (i >= kAhead) {  // output tile
-          const int o = i - kAhead, slot = it % SLOTS, buf = o % NO;
-          ok = wait_for(&sm.full[slot], (it / SLOTS) & 1, abort_flag) &&
-               wait_for(&sm.pfull[o % NP], (o / NP) & 1, abort_flag) &&
-               wait_for(&sm.oempty[buf], ((o / NO) & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = smem_desc<RB>(s0 + slot * C::SLOT, D * 8, 0);
-          const uint64_t b = smem_desc<128>(pb0 + (o % NP) * C::PBYTES, 1024, 1);
-#pragma unroll 1
-          for (int c = 0; c < MT; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              umma_f8(tmem + C::O_COL + (buf * MT + c) * N2, a + c * (8 * RB / 16) + k * (2 * D),
-                      b + 2 * k, id_o, k > 0);
-          umma_commit(&sm.ofull[buf]);
-          umma_commit(&sm.empty[slot]);
-          umma_commit(&sm.pempty[o % NP]);
-          ++it;
-        }
+    if (!ok && lane == 0) {
+      fail();
+      // copies in flight land before the CTA ends
+      for (int s = 0; s < SLOTS; ++s) {
+        mbar_wait_timed(&sm.kfull[s], (k_fills >> s & 1) ^ 1);
+        mbar_wait_timed(&sm.vfull[s], (v_fills >> s & 1) ^ 1);
       }
-      if (!ok) fail();
-      umma_commit(&sm.drain);
-      if (!mbar_wait_timed(&sm.drain, 0)) record_status(p.status, SD_ERR_TIMEOUT);
     }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------------- score products
+    constexpr uint32_t id = idesc_f8(128, N2, false, false);
+    int slot = 0, buf = 0;
+    uint32_t filled = 0, bphase = 0, items = 0;  // filled: parity of each slot's K fills
+    bool ok = true;
+    for (int i = 0; w.left > 0; ++i) {
+      if (w.first(st)) {
+        ok = wait_for(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
+        ++items;
+      }
+      ok &= wait_for(&sm.kfull[slot], filled >> slot & 1, abort_flag);
+      ok &= wait_for(&sm.sempty[buf], bphase ^ 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t a = smem_desc<RB>(smem_u32(slots) + slot * C::SLOT, D * 8, 1);
+      const uint64_t b = smem_desc<RB>(smem_u32(qbuf) + ((items - 1) % NQ) * C::QBYTES, RB * 8, 1);
+#pragma unroll 1
+      for (int ch = 0; ch < C::CH; ++ch)
+#pragma unroll
+        for (int x = 0; x < RB / 32; ++x)  // addresses in 16-byte units
+          umma_f8(tmem + C::S_COL + buf * N2, a + ch * (8 * RB / 16) + 2 * x,
+                  b + ch * (N2 * RB / 16) + 2 * x, id, ch + x > 0);
+      warp_commit(&sm.sfull[buf]);
+      warp_commit(&sm.empty[slot]);
+      if (w.last()) warp_commit(&sm.qempty[(items - 1) % NQ]);
+      filled ^= 1u << slot;
+      slot += i < kAhead ? 1 : 2;
+      if (slot >= SLOTS) slot -= SLOTS;
+      if (++buf == NS) {
+        buf = 0;
+        bphase ^= 1;
+      }
+      w.next(p);
+    }
+    if (lane == 0 && !ok) fail();
+    warp_commit(&sm.drain[0]);
+    if (lane == 0 && !mbar_wait_timed(&sm.drain[0], 0)) record_status(p.status, SD_ERR_TIMEOUT);
     __syncwarp();
-  } else if (warp < 4) {
+  } else if (warp == 2) {
+    // -------------------------------------------------------------------- output products
+    constexpr uint32_t id = idesc_f8(128, N2, true, true);
+    int slot = min(kAhead + 1, st.left) % SLOTS;
+    uint32_t filled = 0;  // parity of each slot's V fills
+    uint32_t items = 0, nan_rows = 0;
+    const int j_first = sm.rowj[0], j_last = sm.rowj[NR - 1];
+    bool ok = true;
+    for (int i = 0; i < st.left; ++i) {
+      const int ob = i % NO;
+      ok &= wait_for(&sm.vfull[slot], filled >> slot & 1, abort_flag);
+      ok &= wait_for(&sm.pfull[i % NP], (i / NP) & 1, abort_flag);
+      ok &= wait_for(&sm.oempty[ob], ((i / NO) & 1) ^ 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (w.first(st)) nan_rows = 0;
+      if (is_edge(p, w, j_first, j_last))
+        nan_rows |= clean_v<D, NR>(p, w, slots + (size_t)slot * C::SLOT, sm.rowj, lane);
+      tc_fence_after();
+      const uint64_t a = smem_desc<RB>(smem_u32(slots) + slot * C::SLOT, D * 8, 0);
+      // weights: 16 columns x 8 keys in 128 bytes, key groups 128 and column groups 2048 bytes
+      // apart, no swizzle
+      const uint64_t b = smem_desc<0>(smem_u32(pbuf) + (i % NP) * C::PBYTES, 2048, 128 / 16);
+#pragma unroll 1
+      for (int c = 0; c < MT; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          umma_f8(tmem + C::O_COL + (ob * MT + c) * N2, a + c * (8 * RB / 16) + k * (2 * D),
+                  b + k * (4 * 128 / 16), id, k > 0);
+      warp_commit(&sm.ofull[ob]);
+      warp_commit(&sm.empty[slot]);
+      warp_commit(&sm.pempty[i % NP]);
+      filled ^= 1u << slot;
+      slot += i + kAhead + 1 < st.left ? 2 : 1;
+      if (slot >= SLOTS) slot -= SLOTS;
+      if (w.last()) {  // rows with a NaN in a V row that only some queries attend to
+        const int lb = items & 1;
+        ok &= wait_for(&sm.lempty[lb], ((items >> 1) & 1) ^ 1, abort_flag);
+        if (lane == 0) sm.nan_rows[lb] = nan_rows;
+        warp_arrive(&sm.lfull[lb]);
+        ++items;
+      }
+      w.next(p);
+    }
+    if (lane == 0 && !ok) fail();
+    warp_commit(&sm.drain[1]);
+    if (lane == 0 && !mbar_wait_timed(&sm.drain[1], 0)) record_status(p.status, SD_ERR_TIMEOUT);
+    __syncwarp();
+  } else if (warp == 3) {
     // -------------------------------------------------------------------- query splitter
-    // Rows in turn over the two warps, four at a time: scale to at most 256, split, store
-    // swizzled.
+    // Four rows at a time: scale to at most 256, split, store swizzled.  Row r has its high part in
+    // column 16 (r / 8) + r % 8, its low part 8 further.
     uint32_t items = 0;
-    const int half = warp - 2;
     constexpr int E = D / 64;  // pairs a lane holds of a row: elements 2 lane + 64 e
-    while (w.left > 0) {
+    bool ok = true;
+    while (w.left > 0 && ok) {
       const int qb = items % NQ;
       uint8_t *dst = qbuf + qb * C::QBYTES;
 #pragma unroll 1
-      for (int r0 = half; r0 < NR; r0 += 8) {
+      for (int r0 = 0; r0 < NR; r0 += 4) {
         uint32_t x[4][E];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int r = r0 + 2 * u, row = row0 + r;
+          const int r = r0 + u, row = row0 + r;
           const int j = row / p.G, h = w.g * p.G + row % p.G;
           const uint32_t *src = reinterpret_cast<const uint32_t *>(
               p.q + (((size_t)w.b * p.n_q + j) * p.Hq + h) * D);
 #pragma unroll
           for (int e = 0; e < E; ++e) x[u][e] = r < rows ? src[lane + 32 * e] : 0u;
         }
-        if (r0 == half) {  // the loads are on their way
-          const bool free = wait_for(&sm.qempty[qb], ((items / NQ) & 1) ^ 1, abort_flag);
-          if (!__all_sync(0xffffffffu, free)) {
-            if (lane == 0) fail();
-            goto splitter_done;
-          }
+        if (r0 == 0) {  // the first loads are on their way
+          ok = warp_wait(&sm.qempty[qb], ((items / NQ) & 1) ^ 1, abort_flag);
+          if (!ok) break;
         }
 #pragma unroll 1
         for (int u = 0; u < 4; ++u) {
-          const int r = r0 + 2 * u;
+          const int r = r0 + u;
           float m = 0.f;
 #pragma unroll
           for (int e = 0; e < E; ++e) {
@@ -615,6 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
           const int ex = max((int)(__float_as_uint(m) >> 23) - 127 + 1 - 8, -100);
           const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
           if (lane == 0) sm.qs[qb][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
+          const int n = 16 * (r >> 3) + (r & 7);
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             float a = __uint_as_float(x[0][e] << 16), b = __uint_as_float(x[0][e] & 0xffff0000u);
@@ -624,194 +802,170 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
             uint32_t hi, lo;
             split2(a * inv, b * inv, hi, lo);
             const int col = 2 * lane + 64 * e;
-            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, r, col)) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, NR + r, col)) = (uint16_t)lo;
+            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, n, col)) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t *>(dst + tile_byte<RB>(N2, n + 8, col)) = (uint16_t)lo;
           }
 #pragma unroll
-          for (int v = 0; v < 3; ++v)
-#pragma unroll
-            for (int e = 0; e < E; ++e) x[v][e] = x[v + 1][e];
+          for (int e = 0; e < E; ++e) {
+            x[0][e] = x[1][e];
+            x[1][e] = x[2][e];
+            x[2][e] = x[3][e];
+          }
         }
+      }
+      if (!ok) {
+        if (lane == 0) fail();
+        break;
       }
       fence_proxy_async_smem();
       warp_arrive(&sm.qfull[qb]);
       ++items;
-      do {  // to the next item
-        const bool end = w.last();
+      bool end = false;
+      while (!end) {  // to the next item
+        end = w.last();
         w.next(p);
-        if (end) break;
-      } while (true);
+      }
     }
-  splitter_done:;
-  } else if (warp < 4 + 4 * SG) {
+  } else if (warp < 4 + C::SW) {
     // -------------------------------------------------------------------- softmax
-    // Thread = key, eight rows of the warpgroup.
-    const int wg = (warp - 4) >> 2, wq = warp & 3, key = wq * 32 + lane, wr = warp - 4;
-    const int r0 = 8 * wg;
-    const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    // Thread = key, eight rows of the warpgroup, every SETS-th tile.
+    const int grp = (warp - 4) >> 2, set = grp / SG, wg = grp % SG;
+    const int wq = warp & 3, key = wq * 32 + lane, r0 = 8 * wg;
+    const int box = key >> (31 - __clz(p.bk));
+    const uint32_t s_at = tmem + C::S_COL + 2 * r0 + ((uint32_t)(wq * 32) << 16);
     bool bad = false;
-    float m_run = -INFINITY;  // of row r0 + lane
-    float l[8], qsc[8];
+    // l of this thread's keys in the frame 2^F: F follows the maximum in steps of 2^20 and more.
+    // kNone stands for no key (or nothing but NaN) so far.
+    float l[8], F[8], qsc[8];
     uint32_t items = 0;
     const int j_first = sm.rowj[0], j_last = sm.rowj[NR - 1];
     for (int i = 0; w.left > 0; ++i, w.next(p)) {
-      const int buf = i % NS;
-      const int p0 = w.pos(), pos = p0 + key;
-      if (w.first(st)) {
+      const int buf = i % NS, ring = i % kScaleRing;
+      if (__builtin_expect(w.first(st), 0)) {
         // the splitter wrote the rows' scales before the scores were computed
         bad |= !wait_for(&sm.qfull[items % NQ], (items / NQ) & 1, abort_flag);
         ++items;
-        m_run = -INFINITY;
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           l[r] = 0.f;
+          F[r] = kNone;
           qsc[r] = sm.qs[(items - 1) % NQ][r0 + r] * p.scale_log2;
         }
         warp_arrive(&sm.qempty[(items - 1) % NQ]);
       }
-      const int ring = i % kScaleRing;
-      bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
-      const float ks = sm.scales[ring][0][key >> 4];
-      const float vs = fmaxf(sm.scales[ring][1][key >> 4], 0x1p-100f);
-      const bool hole = sm.hole[ring] != 0;
-      warp_arrive(&sm.sc_empty[ring]);
-      const float lvs = log2f(vs), rvs = 1.f / vs;
-      // a tile at a range's end, where not every row attends to every key
-      const bool edge = hole || p0 < row_lo(p, w.s, j_last) ||
-                        p0 + kTile - 1 > row_hi(p, w.s, j_first);
-      bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
-      tc_fence_after();
-      float t[8];
-      {
-        uint32_t hi[8], lo[8];
-        tmem_ld8(tmem + C::S_COL + buf * N2 + r0 + lane_base, hi);
-        tmem_ld8(tmem + C::S_COL + buf * N2 + NR + r0 + lane_base, lo);
-        tmem_ld_wait();
-        tc_fence_before();
-        warp_arrive(&sm.sempty[buf]);
+      if (SETS == 1 || (i & 1) == set) {
+        const int p0 = w.pos();
+        bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
+        const float ks = sm.scales[ring][0][box];
+        const float vs = fmaxf(sm.scales[ring][1][box], 0x1p-80f);
+        const bool edge = is_edge(p, w, j_first, j_last);
+        // the keys of a box that is not there weigh nothing
+        const float lvs = ks < 0.f ? -INFINITY : __log2f(vs), rvs = __frcp_rn(vs);
+        bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
+        tc_fence_after();
+        float t[8];
+        {
+          uint32_t v[16];
+          tmem_ld16(s_at + buf * N2, v);
+          tmem_ld_wait();
+          tc_fence_before();
+          warp_arrive(&sm.sempty[buf]);
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float s = fmaf(__uint_as_float(lo[r]), 0.0625f, __uint_as_float(hi[r]));
-          t[r] = fmaf(s * ks, qsc[r], lvs);
-        }
-      }
-      bool nan_v = false;
-      if (edge) {
-        const bool inside = pos >= w.s.lo && pos <= w.s.hi && ks >= 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int j = sm.rowj[r0 + r];
-          if (!inside || pos < row_lo(p, w.s, j) || pos > row_hi(p, w.s, j)) t[r] = -INFINITY;
-        }
-        // V rows that no query attends to may hold any codes, and 0 * NaN is NaN: they are
-        // cleared; a NaN that only some queries attend to is cleared and goes into their l
-        const bool part =
-            inside && (pos < row_lo(p, w.s, j_last) || pos > row_hi(p, w.s, j_first));
-        const uint32_t vit = min(i + kAhead + 1, st.left) + i;  // V_i in the ring's order
-        bad |= !wait_for(&sm.full[vit % SLOTS], (vit / SLOTS) & 1, abort_flag);
-        uint8_t *v = slots + (size_t)(vit % SLOTS) * C::SLOT + (key >> 3) * (8 * D) + (key & 7) * RB;
-        // bytes 0x7f and 0xff: bit 7 of each such byte
-        auto nan = [](uint32_t z) { return ((z & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
-        if (part)
-#pragma unroll 1
-          for (int u = 0; u < D; u += 16) {
-            const uint4 y = *reinterpret_cast<const uint4 *>(v + u / RB * (8 * RB) +
-                                                             ((u + 16 * lane) & (RB - 1)));
-            nan_v |= (nan(y.x) | nan(y.y) | nan(y.z) | nan(y.w)) != 0;
+          for (int r = 0; r < 8; ++r) {
+            const float s = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
+            t[r] = fmaf(s * ks, qsc[r], lvs);
           }
-        // every warpgroup has seen the codes before the first one clears them
-        bad = barrier_or(1, 128 * SG, bad);
-        if (wg == 0 && !bad && (!inside || (part && nan_v)))
-#pragma unroll 1
-          for (int u = 0; u < D; u += 16) {
-            uint4 *x = reinterpret_cast<uint4 *>(v + u / RB * (8 * RB) +
-                                                 ((u + 16 * lane) & (RB - 1)));
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (inside) {
-              auto clear = [&](uint32_t z) { return z & ~((nan(z) >> 7) * 0xffu); };
-              y = *x;
-              y = make_uint4(clear(y.x), clear(y.y), clear(y.z), clear(y.w));
+        }
+        if (__builtin_expect(edge, 0)) {
+          const int a = p0 + key - (p.is_draft ? w.s.hi : w.s.t0);  // keys up to j = a ...
+          const int b = p.window > 0 ? p0 + key - w.s.t0 + p.window - 1 : INT_MAX;  // ... and from b on
+          const int4 j0 = *reinterpret_cast<const int4 *>(&sm.rowj[r0]);
+          const int4 j1 = *reinterpret_cast<const int4 *>(&sm.rowj[r0 + 4]);
+          const int j[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (j[r] < a || j[r] > b) t[r] = -INFINITY;
+        }
+        // maxima of the tile
+        {
+          const float mx = warp_max8(t);
+          if ((lane & 3) == 0) sm.red[grp][(i / SETS) & 1][wq][lane >> 2] = mx;
+        }
+        bad = barrier_or(3 + grp, 128, bad);
+        if (bad) break;
+        float tm[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int h = 0; h < 8; h += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sm.red[grp][(i / SETS) & 1][q][h]);
+            tm[h] = q ? fmaxf(tm[h], x.x) : x.x;
+            tm[h + 1] = q ? fmaxf(tm[h + 1], x.y) : x.y;
+            tm[h + 2] = q ? fmaxf(tm[h + 2], x.z) : x.z;
+            tm[h + 3] = q ? fmaxf(tm[h + 3], x.w) : x.w;
+          }
+        float d[8];  // log2 of the weights' frame, 2^(maximum - 8), in units of l's
+        bool grow = false;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          tm[r] = fmaxf(tm[r], kNone);
+          d[r] = tm[r] - 8.f - F[r];
+          grow |= d[r] > 12.f;
+        }
+        if (__builtin_expect(grow, 0)) {
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            if (d[r] > -8.f) {
+              l[r] *= ex2_approx(-8.f - d[r]);
+              F[r] = tm[r];
+              d[r] = -8.f;
             }
-            *x = y;
+        }
+        bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
+        if (wq == 0) {
+          // tile i - 4's maxima are read: tile i - 2's output product, which this thread has seen
+          // finish, waited for tile i - 4's output to be read
+          if (lane == 0) {
+            float4 *x = reinterpret_cast<float4 *>(&sm.tm[i & 3][r0]);
+            x[0] = make_float4(tm[0], tm[1], tm[2], tm[3]);
+            x[1] = make_float4(tm[4], tm[5], tm[6], tm[7]);
           }
-      }
-      // maxima of the tile: lane r ends up with row r's
-      {
-        float mx = -INFINITY;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const float v = redux_max(t[r]);
-          if (lane == r) mx = v;
+          warp_arrive(&sm.tmfull[i & 3]);
         }
-        if (lane < 8) sm.red[wg][i & 1][wq][lane] = mx;
-      }
-      bad = barrier_or(2 + wg, 128, bad);
-      if (bad) break;
-      if (lane < 8) {
-        float tm = sm.red[wg][i & 1][0][lane];
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int q = 1; q < 4; ++q) tm = fmaxf(tm, sm.red[wg][i & 1][q][lane]);
-        if (tm != tm) tm = 0.f;  // nothing but NaN: the weights are, and l and O become NaN
-        const float m_new = fmaxf(m_run, tm);
-        const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
-        const float beta = tm == -INFINITY ? 0.f : ex2_approx(tm - m_new) * 0x1p-8f;
-        m_run = m_new;
-        sm.row[wr][0][lane] = tm == -INFINITY ? 0.f : tm - 8.f;
-        sm.row[wr][1][lane] = alpha;
-        sm.row[wr][2][lane] = beta;
-      }
-      __syncwarp();
-      bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
-      if (wq == 0) {
-        // tile i - 4's pair is read: tile i - 2's output product, which this thread has seen
-        // finish, waited for tile i - 4's output to be read
-        if (lane < 8)
-          sm.ab[i & 3][r0 + lane] = make_float2(sm.row[wr][1][lane], sm.row[wr][2][lane]);
-        warp_arrive(&sm.abfull[i & 3]);
-      }
-      uint8_t *pd = pbuf + (i % NP) * C::PBYTES;
+        for (int r = 0; r < 8; r += 2) {
+          float wt[2];
 #pragma unroll
-      for (int r = 0; r < 8; r += 2) {
-        const float2 mx = *reinterpret_cast<const float2 *>(&sm.row[wr][0][r]);
-        const float2 al = *reinterpret_cast<const float2 *>(&sm.row[wr][1][r]);
-        const float2 be = *reinterpret_cast<const float2 *>(&sm.row[wr][2][r]);
-        const float w0 = ex2_approx(t[r] - mx.x), w1 = ex2_approx(t[r + 1] - mx.y);
-        float f0 = rvs, f1 = rvs;
-        if (nan_v) {
-          if (t[r] != -INFINITY) f0 = __int_as_float(0x7fc00000);
-          if (t[r + 1] != -INFINITY) f1 = __int_as_float(0x7fc00000);
+          for (int u = 0; u < 2; ++u) {
+            wt[u] = ex2_approx(t[r + u] - (tm[r + u] - 8.f));
+            l[r + u] = fmaf(wt[u], rvs * ex2_approx(d[r + u]), l[r + u]);
+          }
+          split2(wt[0], wt[1], hi[r / 2], lo[r / 2]);
         }
-        l[r] = fmaf(l[r], al.x, w0 * f0 * be.x);
-        l[r + 1] = fmaf(l[r + 1], al.y, w1 * f1 * be.y);
-        uint32_t hi, lo;
-        split2(w0, w1, hi, lo);
-        pd[tile_byte<128>(N2, r0 + r, key)] = (uint8_t)hi;
-        pd[tile_byte<128>(N2, r0 + r + 1, key)] = (uint8_t)(hi >> 8);
-        pd[tile_byte<128>(N2, NR + r0 + r, key)] = (uint8_t)lo;
-        pd[tile_byte<128>(N2, NR + r0 + r + 1, key)] = (uint8_t)(lo >> 8);
+        *reinterpret_cast<uint4 *>(pbuf + (i % NP) * C::PBYTES + wg * 2048 + key * 16) =
+            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                       lo[2] | lo[3] << 16);
+        fence_proxy_async_smem();
+        warp_arrive(&sm.pfull[i % NP]);
       }
-      fence_proxy_async_smem();
-      warp_arrive(&sm.pfull[i % NP]);
-      if (w.last()) {
-        // l over the 128 keys; lane r of the warpgroup's first warp hands (m, l) of row r over
+      if (__builtin_expect(w.last(), 0)) {
+        // l over the 128 keys; lane r of the warpgroup's first warp hands (F, l) of row r over
         const int lb = (items - 1) & 1;
         bad |= !wait_for(&sm.lempty[lb], (((items - 1) >> 1) & 1) ^ 1, abort_flag);
-        float mine = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          float v = l[r];
-          for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == r) mine = v;
-        }
-        float (&red)[4][8] = sm.red[wg][(i & 1) ^ 1];
-        if (lane < 8) red[wq][lane] = mine;
-        bad = barrier_or(2 + wg, 128, bad);
+        float (&red)[4][8] = sm.red[grp][0];
+        bad = barrier_or(3 + grp, 128, bad);  // its maxima are read
         if (bad) break;
-        if (wq == 0 && lane < 8)
-          sm.ml[lb][r0 + lane] =
-              make_float2(m_run, red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]);
+        const float sum = warp_sum8(l);
+        if ((lane & 3) == 0) red[wq][lane >> 2] = sum;
+        bad = barrier_or(3 + grp, 128, bad);
+        if (wq == 0 && lane == 0)
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            sm.ml[lb][set][r0 + r] =
+                make_float2(F[r], red[0][r] + red[1][r] + red[2][r] + red[3][r]);
         // the next tile writes there again: not before the first warp has read it
-        bad = barrier_or(2 + wg, 128, bad);
+        bad = barrier_or(3 + grp, 128, bad);
         warp_arrive(&sm.lfull[lb]);
         if (bad) break;
       }
@@ -819,11 +973,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     if (bad && lane == 0) fail();
   } else {
     // -------------------------------------------------------------------- joining warps
-    const int jg = (warp - 4 - 4 * SG) >> 2, wq = warp & 3, col = wq * 32 + lane;
+    const int jg = (warp - 4 - C::SW) >> 2, wq = warp & 3, col = wq * 32 + lane;
     const int c0 = jg * MJ;  // first chunk of the warpgroup
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
     bool ok = true;
     float acc[MJ][NR];
+    float m_run = kNone;  // of row `lane`
     uint32_t items = 0;
     bool whole = false;
     for (int i = 0; w.left > 0; ++i, w.next(p)) {
@@ -831,61 +986,88 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       if (w.first(st)) {
         whole = w.tau == 0 && w.left >= w.s.n;
         ++items;
+        m_run = kNone;
 #pragma unroll
         for (int c = 0; c < MJ; ++c)
 #pragma unroll
           for (int r = 0; r < NR; ++r) acc[c][r] = 0.f;
       }
-      ok = wait_for(&sm.abfull[i & 3], (i >> 2) & 1, abort_flag) &&
-           wait_for(&sm.ofull[buf], (i / NO) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(&sm.tmfull[i & 3], (i >> 2) & 1, abort_flag) &&
+           warp_wait(&sm.ofull[buf], (i / NO) & 1, abort_flag);
       if (!ok) break;
       tc_fence_after();
+      const float tm = lane < NR ? sm.tm[i & 3][lane] : kNone;
+      const float m_new = fmaxf(m_run, tm);
+      const float alpha = ex2_approx(m_run - m_new);
+      float *const beta = sm.beta[warp - 4 - C::SW];
+      if (lane < NR) beta[lane] = ex2_approx(tm - m_new) * 0x1p-8f;
+      m_run = m_new;
+      __syncwarp();
       if (D >= 128 || wq < 2) {
         const uint32_t o0 = tmem + C::O_COL + (buf * MT + c0) * N2 + lane_base;
+        // only the first few tiles of an item raise a maximum
+        if (__builtin_expect(__any_sync(0xffffffffu, alpha != 1.f), 0))
 #pragma unroll
-        for (int c = 0; c < MJ; ++c)
+          for (int r = 0; r < NR; ++r) {
+            const float al = __shfl_sync(0xffffffffu, alpha, r);
 #pragma unroll
-          for (int r = 0; r < NR; r += 8) {
-            uint32_t hi[8], lo[8];
-            tmem_ld8(o0 + c * N2 + r, hi);
-            tmem_ld8(o0 + c * N2 + NR + r, lo);
+            for (int c = 0; c < MJ; ++c) acc[c][r] *= al;
+          }
+#pragma unroll
+        for (int r = 0; r < NR; r += 8) {
+          float be[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) be[e] = beta[r + e];
+#pragma unroll
+          for (int c = 0; c < MJ; ++c) {
+            uint32_t v[16];
+            tmem_ld16(o0 + c * N2 + 2 * r, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 ab = sm.ab[i & 3][r + e];
-              const float o = fmaf(__uint_as_float(lo[e]), 0.0625f, __uint_as_float(hi[e]));
-              acc[c][r + e] = fmaf(acc[c][r + e], ab.x, o * ab.y);
-            }
+            for (int e = 0; e < 8; ++e)
+              acc[c][r + e] = fmaf(
+                  fmaf(__uint_as_float(v[8 + e]), 0.0625f, __uint_as_float(v[e])), be[e],
+                  acc[c][r + e]);
           }
+        }
       }
       tc_fence_before();
       warp_arrive(&sm.oempty[buf]);
-      if (!w.last()) continue;
+      if (__builtin_expect(!w.last(), 1)) continue;
       const int lb = (items - 1) & 1;
-      ok = wait_for(&sm.lfull[lb], ((items - 1) >> 1) & 1, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      ok = warp_wait(&sm.lfull[lb], ((items - 1) >> 1) & 1, abort_flag);
       if (!ok) break;
-      const size_t item = (size_t)w.b * p.Hkv + w.g;
+      // l of row `lane` in this warp's frame
+      float l = 0.f;
+      if (lane < NR)
+#pragma unroll
+        for (int s = 0; s < SETS; ++s) {
+          const float2 x = sm.ml[lb][s][lane];
+          l = fmaf(x.y, ex2_approx(x.x - m_run), l);
+        }
+      if (sm.nan_rows[lb] >> lane & 1) l = __int_as_float(0x7fc00000);
+      // lane r: where row r goes and its factor
+      const int jr = sm.rowj[min(lane, NR - 1)], row = row0 + lane;
+      const size_t item = (size_t)w.b * p.Hkv + w.g, at = (item + cta) * (size_t)(p.R * p.RG) + row;
+      const float scale = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // no key: a zero row
+      const unsigned long long to =
+          whole ? (unsigned long long)(p.out + (((size_t)w.b * p.n_q + jr) * p.Hq + w.g * p.G + row -
+                                                (size_t)jr * p.G) * D)
+                : (unsigned long long)(p.ws_o + at * D);
+      if (!whole && jg == 0 && wq == 0 && lane < rows)
+        *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m_run, l);
       if (D >= 128 || wq < 2) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
+          const float f = __shfl_sync(0xffffffffu, scale, r);
+          const unsigned long long dst = __shfl_sync(0xffffffffu, to, r);
           if (r >= rows) continue;
-          const float2 ml = sm.ml[lb][r];
-          const int row = row0 + r, j = sm.rowj[r];
-          if (whole) {
-            const float inv = ml.y != 0.f ? 1.f / ml.y : 0.f;  // no key: a zero row
-            __nv_bfloat16 *dst =
-                p.out + (((size_t)w.b * p.n_q + j) * p.Hq + w.g * p.G + row - j * p.G) * D;
 #pragma unroll
-            for (int c = 0; c < MJ; ++c)
-              dst[(c0 + c) * 128 + col] = __float2bfloat16_rn(acc[c][r] * inv);
-          } else {
-            const size_t at = (item + cta) * (size_t)(p.R * p.RG) + row;
-#pragma unroll
-            for (int c = 0; c < MJ; ++c) p.ws_o[at * D + (c0 + c) * 128 + col] = acc[c][r];
-            if (jg == 0 && wq == 0 && lane == 0)
-              *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = ml;
+          for (int c = 0; c < MJ; ++c) {
+            const float v = acc[c][r] * f;
+            const int d = (c0 + c) * 128 + col;
+            if (whole) reinterpret_cast<__nv_bfloat16 *>(dst)[d] = __float2bfloat16_rn(v);
+            else reinterpret_cast<float *>(dst)[d] = v;
           }
         }
       }
@@ -933,7 +1115,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
   const int c0 = (int)share_of(total, first, P), c1 = (int)share_of(total, first + n - 1, P);
   if (c0 == c1) return;  // written by its only CTA
   const size_t pitch = (size_t)p.R * p.RG;
-  float m = -INFINITY, den = 0.f;
+  float m = kNone, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   // runs of 8 partials: their loads are on their way together
   for (int c = c0; c <= c1; c += 8) {
@@ -945,15 +1127,14 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
       const bool held = x <= c1;
       const size_t at = ((size_t)item + x) * pitch + row;
       ml[u] = held ? *reinterpret_cast<const float2 *>(p.ws_ml + at * 2)
-                   : make_float2(-INFINITY, 0.f);
+                   : make_float2(kNone, 0.f);
       o[u] = held && d < p.D ? __ldcg(reinterpret_cast<const float4 *>(p.ws_o + at * p.D + d))
                              : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float mx = m;
 #pragma unroll
     for (int u = 0; u < 8; ++u) mx = fmaxf(mx, ml[u].x);
-    if (mx == -INFINITY) continue;
-    const float a = ex2_approx(m - mx);  // 0 from -inf
+    const float a = ex2_approx(m - mx);
     den *= a;
     acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
     m = mx;
@@ -1064,6 +1245,7 @@ static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const voi
   p.q_offset = d->q_offset;
   p.bk = p.bs % 128 == 0 ? 128 : p.bs % 64 == 0 ? 64 : p.bs % 32 == 0 ? 32 : 16;
   p.box_bytes = p.bk * p.D;
+  p.row_groups = (int)((long long)p.num_blocks * p.Hkv * p.bs / 8);
   p.R = r.R;
   p.RG = r.RG;
   p.P = ctas(r);

@@ -55,6 +55,7 @@ struct Params {
   __nv_bfloat16 *out;
   float *ws_o;   // [slots][R * RG][D]
   float *ws_ml;  // [slots][R * RG][2]
+  int4 *ws_rec;  // [P] items to join
   int *status;
 };
 
@@ -109,6 +110,37 @@ struct Start {
   int b, g, tau;
   int left;  // tiles
 };
+
+// Tiles of all items (one warp).
+__device__ __forceinline__ unsigned total_tiles(const Params &p, int lane, bool report) {
+  unsigned total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const unsigned n = b0 + lane < p.B ? seq_of(p, b0 + lane, report).n : 0;
+    total += __reduce_add_sync(0xffffffffu, n) * p.Hkv;
+  }
+  return total;
+}
+// Item and tile of place ``at`` of the flattened list (one warp; at < total).
+__device__ __forceinline__ Start locate(const Params &p, unsigned at, int lane) {
+  unsigned pre = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const unsigned n = b0 + lane < p.B ? seq_of(p, b0 + lane, false).n : 0;
+    unsigned v = n * p.Hkv;
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, at < pre + v);
+    if (m) {
+      const int src = __ffs(m) - 1;
+      const unsigned off = at - pre - __shfl_sync(0xffffffffu, v - n * p.Hkv, src);
+      const unsigned nn = __shfl_sync(0xffffffffu, n, src);
+      return Start{b0 + src, (int)(off / nn), (int)(off % nn), 0};
+    }
+    pre += __shfl_sync(0xffffffffu, v, 31);
+  }
+  return Start{0, 0, 0, 0};
+}
 
 // Walks the tiles of a CTA; every role walks the same ones.
 struct Walk {
@@ -200,11 +232,7 @@ struct Cfg {
   static constexpr int SG = NR / 8;
   static constexpr int MJ = MT * NR <= 48 ? MT : MT / 2 * NR <= 48 ? MT / 2 : 1;
   static constexpr int JG = MT / MJ;                  // joining warpgroups, MJ chunks each
-  // Softmax warpgroups in two sets that take the tiles in turn where one tile's chain of waits,
-  // exchange and rounding takes longer than the tile's bytes.
-  static constexpr int SETS = D < 512 && NR <= 8 ? 2 : 1;
-  static constexpr int SW = 4 * SG * SETS;            // softmax warps
-  static constexpr int THREADS = 32 * (4 + SW) + 128 * JG;
+  static constexpr int THREADS = 128 * (1 + SG + JG);
   static constexpr int SLOT = kTile * D;
   static constexpr int NQ = D == 512 ? 1 : 2;         // query buffers
   static constexpr int NP = D == 512 && NR == 24 ? 1 : 2;  // weight buffers
@@ -220,10 +248,10 @@ struct Cfg {
   static_assert(COLS <= 512, "tensor memory");
   struct Small {
     alignas(16) float scales[kScaleRing][2][8];  // K's and V's of each box of a tile; -1: no such box
-    alignas(16) float red[SETS * SG][2][4][8];
+    alignas(16) float red[SG][2][4][8];
     alignas(16) float tm[4][NR];          // tile maxima for the joining warps
     alignas(16) float beta[4 * JG][NR];   // their factors of a tile, by warp
-    float2 ml[2][SETS][NR];   // frame and l of an item
+    float2 ml[2][NR];         // frame and l of an item
     float qs[2][NR];          // 2^e scale of the query rows
     uint32_t nan_rows[2];     // of an item
     alignas(16) int rowj[NR];             // query position of a row (row / G)
@@ -494,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Params p) {
   using C = Cfg<D, NR>;
   constexpr int N2 = C::N2, MT = C::MT, RB = C::RB, SLOTS = C::SLOTS, NQ = C::NQ, NP = C::NP,
-                NO = C::NO, NS = C::NS, SG = C::SG, SETS = C::SETS, MJ = C::MJ;
+                NO = C::NO, NS = C::NS, SG = C::SG, MJ = C::MJ;
   extern __shared__ uint8_t smem_raw[];
   // aligned by pointer arithmetic, so that the compiler still knows it for shared memory (through an
   // integer cast every access becomes a generic one with 64-bit addresses: B 64 at D 256, 252 us
@@ -523,12 +551,12 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.qfull[i], 1);
-      mbar_init(&sm.qempty[i], 1 + C::SW);  // the item's last scores; its row scales are read
+      mbar_init(&sm.qempty[i], 1 + 4 * SG);  // the item's last scores; its row scales are read
       mbar_init(&sm.pfull[i], 4 * SG);
       mbar_init(&sm.pempty[i], 1);
       mbar_init(&sm.ofull[i], 1);
       mbar_init(&sm.oempty[i], 4 * C::JG);
-      mbar_init(&sm.lfull[i], C::SW + 1);
+      mbar_init(&sm.lfull[i], 4 * SG + 1);
       mbar_init(&sm.lempty[i], 4 * C::JG);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sm.tmfull[i], SG);
@@ -546,39 +574,22 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   pdl_wait();
   if (warp == 0) {
     // where this CTA's share of the T tiles begins
-    unsigned total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      const unsigned n = b < p.B ? seq_of(p, b, blockIdx.x == 0).n : 0;
-      total += __reduce_add_sync(0xffffffffu, n) * p.Hkv;
-    }
+    const unsigned total = total_tiles(p, lane, blockIdx.x == 0);
     const unsigned P = min((unsigned)p.P, total);
     Start st{0, 0, 0, 0};
-    unsigned at = 0;
     if ((unsigned)cta < P) {
-      at = share(total, cta, P);
+      const unsigned at = share(total, cta, P);
+      st = locate(p, at, lane);
       st.left = (int)(share(total, cta + 1, P) - at);
     }
-    unsigned pre = 0;
-    for (int b0 = 0; b0 < p.B && st.left > 0; b0 += 32) {
-      const int b = b0 + lane;
-      const unsigned n = b < p.B ? seq_of(p, b, false).n : 0;
-      unsigned v = n * p.Hkv;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+    if (rg == 0) {  // the item whose first border inside is this share's begin
+      int last = -1;
+      if (st.tau > 0) {
+        const unsigned first = share(total, cta, P) - st.tau;
+        if (share_of(total, first, P) + 1 == (unsigned)cta)
+          last = (int)share_of(total, first + seq_of(p, st.b, false).n - 1, P);
       }
-      const unsigned m = __ballot_sync(0xffffffffu, at < pre + v);
-      if (m) {
-        const int src = __ffs(m) - 1;
-        const unsigned before = pre + __shfl_sync(0xffffffffu, v - n * p.Hkv, src);
-        const unsigned nn = __shfl_sync(0xffffffffu, n, src);
-        st.b = b0 + src;
-        st.g = (int)((at - before) / nn);
-        st.tau = (int)((at - before) % nn);
-        break;
-      }
-      pre += __shfl_sync(0xffffffffu, v, 31);
+      if (lane == 0) p.ws_rec[cta] = make_int4(st.b, st.g, last, 0);
     }
     if (lane == 0) sm.start = st;
   }
@@ -826,10 +837,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         w.next(p);
       }
     }
-  } else if (warp < 4 + C::SW) {
+  } else if (warp < 4 + 4 * SG) {
     // -------------------------------------------------------------------- softmax
-    // Thread = key, eight rows of the warpgroup, every SETS-th tile.
-    const int grp = (warp - 4) >> 2, set = grp / SG, wg = grp % SG;
+    // Thread = key, eight rows of the warpgroup.
+    const int wg = (warp - 4) >> 2;
     const int wq = warp & 3, key = wq * 32 + lane, r0 = 8 * wg;
     const int box = key >> (31 - __clz(p.bk));
     const uint32_t s_at = tmem + C::S_COL + 2 * r0 + ((uint32_t)(wq * 32) << 16);
@@ -853,119 +864,115 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         }
         warp_arrive(&sm.qempty[(items - 1) % NQ]);
       }
-      if (SETS == 1 || (i & 1) == set) {
-        const int p0 = w.pos();
-        bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
-        const float ks = sm.scales[ring][0][box];
-        const float vs = fmaxf(sm.scales[ring][1][box], 0x1p-80f);
-        const bool edge = is_edge(p, w, j_first, j_last);
-        // the keys of a box that is not there weigh nothing
-        const float lvs = ks < 0.f ? -INFINITY : __log2f(vs), rvs = __frcp_rn(vs);
-        bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
-        tc_fence_after();
-        float t[8];
-        {
-          uint32_t v[16];
-          tmem_ld16(s_at + buf * N2, v);
-          tmem_ld_wait();
-          tc_fence_before();
-          warp_arrive(&sm.sempty[buf]);
-#pragma unroll
-          for (int r = 0; r < 8; ++r) {
-            const float s = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
-            t[r] = fmaf(s * ks, qsc[r], lvs);
-          }
-        }
-        if (__builtin_expect(edge, 0)) {
-          const int a = p0 + key - (p.is_draft ? w.s.hi : w.s.t0);  // keys up to j = a ...
-          const int b = p.window > 0 ? p0 + key - w.s.t0 + p.window - 1 : INT_MAX;  // ... and from b on
-          const int4 j0 = *reinterpret_cast<const int4 *>(&sm.rowj[r0]);
-          const int4 j1 = *reinterpret_cast<const int4 *>(&sm.rowj[r0 + 4]);
-          const int j[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (j[r] < a || j[r] > b) t[r] = -INFINITY;
-        }
-        // maxima of the tile
-        {
-          const float mx = warp_max8(t);
-          if ((lane & 3) == 0) sm.red[grp][(i / SETS) & 1][wq][lane >> 2] = mx;
-        }
-        bad = barrier_or(3 + grp, 128, bad);
-        if (bad) break;
-        float tm[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int h = 0; h < 8; h += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sm.red[grp][(i / SETS) & 1][q][h]);
-            tm[h] = q ? fmaxf(tm[h], x.x) : x.x;
-            tm[h + 1] = q ? fmaxf(tm[h + 1], x.y) : x.y;
-            tm[h + 2] = q ? fmaxf(tm[h + 2], x.z) : x.z;
-            tm[h + 3] = q ? fmaxf(tm[h + 3], x.w) : x.w;
-          }
-        float d[8];  // log2 of the weights' frame, 2^(maximum - 8), in units of l's
-        bool grow = false;
+      const int p0 = w.pos();
+      bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
+      const float ks = sm.scales[ring][0][box];
+      const float vs = fmaxf(sm.scales[ring][1][box], 0x1p-80f);
+      const bool edge = is_edge(p, w, j_first, j_last);
+      // the keys of a box that is not there weigh nothing
+      const float lvs = ks < 0.f ? -INFINITY : __log2f(vs), rvs = __frcp_rn(vs);
+      bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
+      tc_fence_after();
+      float t[8];
+      {
+        uint32_t v[16];
+        tmem_ld16(s_at + buf * N2, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        warp_arrive(&sm.sempty[buf]);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          tm[r] = fmaxf(tm[r], kNone);
-          d[r] = tm[r] - 8.f - F[r];
-          grow |= d[r] > 12.f;
+          const float s = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
+          t[r] = fmaf(s * ks, qsc[r], lvs);
         }
-        if (__builtin_expect(grow, 0)) {
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            if (d[r] > -8.f) {
-              l[r] *= ex2_approx(-8.f - d[r]);
-              F[r] = tm[r];
-              d[r] = -8.f;
-            }
-        }
-        bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
-        if (wq == 0) {
-          // tile i - 4's maxima are read: tile i - 2's output product, which this thread has seen
-          // finish, waited for tile i - 4's output to be read
-          if (lane == 0) {
-            float4 *x = reinterpret_cast<float4 *>(&sm.tm[i & 3][r0]);
-            x[0] = make_float4(tm[0], tm[1], tm[2], tm[3]);
-            x[1] = make_float4(tm[4], tm[5], tm[6], tm[7]);
-          }
-          warp_arrive(&sm.tmfull[i & 3]);
-        }
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int r = 0; r < 8; r += 2) {
-          float wt[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            wt[u] = ex2_approx(t[r + u] - (tm[r + u] - 8.f));
-            l[r + u] = fmaf(wt[u], rvs * ex2_approx(d[r + u]), l[r + u]);
-          }
-          split2(wt[0], wt[1], hi[r / 2], lo[r / 2]);
-        }
-        *reinterpret_cast<uint4 *>(pbuf + (i % NP) * C::PBYTES + wg * 2048 + key * 16) =
-            make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
-                       lo[2] | lo[3] << 16);
-        fence_proxy_async_smem();
-        warp_arrive(&sm.pfull[i % NP]);
       }
+      if (__builtin_expect(edge, 0)) {
+        const int a = p0 + key - (p.is_draft ? w.s.hi : w.s.t0);  // keys up to j = a ...
+        const int b = p.window > 0 ? p0 + key - w.s.t0 + p.window - 1 : INT_MAX;  // ... and from b on
+        const int4 j0 = *reinterpret_cast<const int4 *>(&sm.rowj[r0]);
+        const int4 j1 = *reinterpret_cast<const int4 *>(&sm.rowj[r0 + 4]);
+        const int j[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (j[r] < a || j[r] > b) t[r] = -INFINITY;
+      }
+      // maxima of the tile
+      {
+        const float mx = warp_max8(t);
+        if ((lane & 3) == 0) sm.red[wg][i & 1][wq][lane >> 2] = mx;
+      }
+      bad = barrier_or(1 + wg, 128, bad);
+      if (bad) break;
+      float tm[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(&sm.red[wg][i & 1][q][h]);
+          tm[h] = q ? fmaxf(tm[h], x.x) : x.x;
+          tm[h + 1] = q ? fmaxf(tm[h + 1], x.y) : x.y;
+          tm[h + 2] = q ? fmaxf(tm[h + 2], x.z) : x.z;
+          tm[h + 3] = q ? fmaxf(tm[h + 3], x.w) : x.w;
+        }
+      float d[8];  // log2 of the weights' frame, 2^(maximum - 8), in units of l's
+      bool grow = false;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        tm[r] = fmaxf(tm[r], kNone);
+        d[r] = tm[r] - 8.f - F[r];
+        grow |= d[r] > 12.f;
+      }
+      if (__builtin_expect(grow, 0)) {
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (d[r] > -8.f) {
+            l[r] *= ex2_approx(-8.f - d[r]);
+            F[r] = tm[r];
+            d[r] = -8.f;
+          }
+      }
+      bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
+      if (wq == 0) {
+        // tile i - 4's maxima are read: tile i - 2's output product, which this thread has seen
+        // finish, waited for tile i - 4's output to be read
+        if (lane == 0) {
+          float4 *x = reinterpret_cast<float4 *>(&sm.tm[i & 3][r0]);
+          x[0] = make_float4(tm[0], tm[1], tm[2], tm[3]);
+          x[1] = make_float4(tm[4], tm[5], tm[6], tm[7]);
+        }
+        warp_arrive(&sm.tmfull[i & 3]);
+      }
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int r = 0; r < 8; r += 2) {
+        float wt[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          wt[u] = ex2_approx(t[r + u] - (tm[r + u] - 8.f));
+          l[r + u] = fmaf(wt[u], rvs * ex2_approx(d[r + u]), l[r + u]);
+        }
+        split2(wt[0], wt[1], hi[r / 2], lo[r / 2]);
+      }
+      *reinterpret_cast<uint4 *>(pbuf + (i % NP) * C::PBYTES + wg * 2048 + key * 16) =
+          make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16,
+                     lo[2] | lo[3] << 16);
+      fence_proxy_async_smem();
+      warp_arrive(&sm.pfull[i % NP]);
       if (__builtin_expect(w.last(), 0)) {
         // l over the 128 keys; lane r of the warpgroup's first warp hands (F, l) of row r over
         const int lb = (items - 1) & 1;
         bad |= !wait_for(&sm.lempty[lb], (((items - 1) >> 1) & 1) ^ 1, abort_flag);
-        float (&red)[4][8] = sm.red[grp][0];
-        bad = barrier_or(3 + grp, 128, bad);  // its maxima are read
-        if (bad) break;
+        float (&red)[4][8] = sm.red[wg][(i & 1) ^ 1];
         const float sum = warp_sum8(l);
         if ((lane & 3) == 0) red[wq][lane >> 2] = sum;
-        bad = barrier_or(3 + grp, 128, bad);
+        bad = barrier_or(1 + wg, 128, bad);
         if (wq == 0 && lane == 0)
 #pragma unroll
           for (int r = 0; r < 8; ++r)
-            sm.ml[lb][set][r0 + r] =
+            sm.ml[lb][r0 + r] =
                 make_float2(F[r], red[0][r] + red[1][r] + red[2][r] + red[3][r]);
         // the next tile writes there again: not before the first warp has read it
-        bad = barrier_or(3 + grp, 128, bad);
+        bad = barrier_or(1 + wg, 128, bad);
         warp_arrive(&sm.lfull[lb]);
         if (bad) break;
       }
@@ -973,9 +980,15 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     if (bad && lane == 0) fail();
   } else {
     // -------------------------------------------------------------------- joining warps
-    const int jg = (warp - 4 - C::SW) >> 2, wq = warp & 3, col = wq * 32 + lane;
+    const int jg = (warp - 4 - 4 * SG) >> 2, wq = warp & 3, col = wq * 32 + lane;
     const int c0 = jg * MJ;  // first chunk of the warpgroup
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+    // sequences with no key at all: zero rows
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+      if (seq_of(p, b, false).n == 0)
+        for (int e = tid - 128 * (1 + SG); e < p.n_q * p.Hq * (D / 8); e += 128 * C::JG)
+          reinterpret_cast<uint4 *>(p.out)[(size_t)b * p.n_q * p.Hq * (D / 8) + e] =
+              make_uint4(0, 0, 0, 0);
     bool ok = true;
     float acc[MJ][NR];
     float m_run = kNone;  // of row `lane`
@@ -999,7 +1012,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       const float tm = lane < NR ? sm.tm[i & 3][lane] : kNone;
       const float m_new = fmaxf(m_run, tm);
       const float alpha = ex2_approx(m_run - m_new);
-      float *const beta = sm.beta[warp - 4 - C::SW];
+      float *const beta = sm.beta[warp - 4 - 4 * SG];
       if (lane < NR) beta[lane] = ex2_approx(tm - m_new) * 0x1p-8f;
       m_run = m_new;
       __syncwarp();
@@ -1039,12 +1052,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       if (!ok) break;
       // l of row `lane` in this warp's frame
       float l = 0.f;
-      if (lane < NR)
-#pragma unroll
-        for (int s = 0; s < SETS; ++s) {
-          const float2 x = sm.ml[lb][s][lane];
-          l = fmaf(x.y, ex2_approx(x.x - m_run), l);
-        }
+      if (lane < NR) {
+        const float2 x = sm.ml[lb][lane];
+        l = x.y * ex2_approx(x.x - m_run);
+      }
       if (sm.nan_rows[lb] >> lane & 1) l = __int_as_float(0x7fc00000);
       // lane r: where row r goes and its factor
       const int jr = sm.rowj[min(lane, NR - 1)], row = row0 + lane;
@@ -1081,39 +1092,18 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem, C::TMEM);
 }
 
-// Joins the partials of items that several CTAs shared, in CTA order; zero rows for sequences
-// with no keys.  One CTA per (item, row), 4 columns a thread.
+// Joins the partials of items that several CTAs shared, in CTA order.  One CTA per (border between two
+// shares, row), 4 columns a thread; the attention kernel left a record of the item whose first border
+// it is.
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Params p) {
   pdl_wait();
-  const int item = blockIdx.x, row = blockIdx.y;
-  const int b = item / p.Hkv, g = item % p.Hkv;
-  __shared__ unsigned s_pre, s_total;
-  if (threadIdx.x < 32) {
-    unsigned pre = 0, total = 0;
-    for (int i = threadIdx.x; i < p.B; i += 32) {
-      const unsigned n = seq_of(p, i, false).n * p.Hkv;
-      total += n;
-      if (i < b) pre += n;
-    }
-    pre = __reduce_add_sync(0xffffffffu, pre);
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (threadIdx.x == 0) {
-      s_pre = pre;
-      s_total = total;
-    }
-  }
-  const unsigned n = seq_of(p, b, false).n;
-  __syncthreads();
+  const int4 rec = p.ws_rec[blockIdx.x + 1];  // sequence, kv head, last share; -1: nothing here
+  if (rec.z < 0) return;
+  const int b = rec.x, g = rec.y, c0 = blockIdx.x, c1 = rec.z, row = blockIdx.y;
+  const int item = b * p.Hkv + g;
   __nv_bfloat16 *dst =
       p.out + (((size_t)b * p.n_q + row / p.G) * p.Hq + g * p.G + row % p.G) * p.D;
   const int d = threadIdx.x * 4;
-  if (n == 0) {
-    if (d < p.D) *reinterpret_cast<uint2 *>(dst + d) = make_uint2(0, 0);
-    return;
-  }
-  const unsigned total = s_total, P = min((unsigned)p.P, total), first = s_pre + g * n;
-  const int c0 = (int)share_of(total, first, P), c1 = (int)share_of(total, first + n - 1, P);
-  if (c0 == c1) return;  // written by its only CTA
   const size_t pitch = (size_t)p.R * p.RG;
   float m = kNone, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1213,7 +1203,7 @@ static size_t ws_o_bytes(const sd_attn_desc *d, const Rows &r) {
 static size_t ws_size(const sd_attn_desc *d) {
   const Rows r = rows_of(d->h_q / d->h_kv * d->n_q, d->head_dim);
   const size_t slots = (size_t)d->batch * d->h_kv + ctas(r);
-  return ws_o_bytes(d, r) + round_up(slots * r.R * r.RG * 8, 256);
+  return ws_o_bytes(d, r) + round_up(slots * r.R * r.RG * 8, 256) + ctas(r) * sizeof(int4);
 }
 
 static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const void *kc,
@@ -1259,6 +1249,8 @@ static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const voi
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
   p.ws_o = reinterpret_cast<float *>(ws);
   p.ws_ml = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ws) + ws_o_bytes(d, r));
+  p.ws_rec = reinterpret_cast<int4 *>(
+      reinterpret_cast<uint8_t *>(ws) + ws_size(d) - (size_t)p.P * sizeof(int4));
   p.status = device_status_word();
   CUtensorMap km, vm;
   const uint64_t rows = (uint64_t)p.num_blocks * p.Hkv * p.bs;
@@ -1274,7 +1266,8 @@ static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const voi
   SDV_CASE(512, 8) SDV_CASE(512, 16) SDV_CASE(512, 24) return SD_ERR_UNSUPPORTED;
 #undef SDV_CASE
   if (e != SD_OK) return e;
-  return cuda_status(launch(combine_kernel, dim3(p.B * p.Hkv, p.M), dim3(128), 0, st, p));
+  if (p.P == 1) return SD_OK;
+  return cuda_status(launch(combine_kernel, dim3(p.P - 1, p.M), dim3(128), 0, st, p));
 }
 
 }  // namespace q8

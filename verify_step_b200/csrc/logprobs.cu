@@ -9,12 +9,14 @@
 // (m, S, A) of two parts merge as S = S_1 w_1 + S_2 w_2, A = sum w_i (A_i + d_i S_i) with d_i the
 // shift of m_i to the common maximum and w_i = 2^d_i, all in float32.
 //
-// Bound by HBM: the 4 V bytes of a row are read once.  A CTA takes a chunk of 256 * EPT logits of
-// one row into registers and makes three passes over them: maximum, sums, candidates.  The top n
-// are found without sorting: every thread's largest (logit, id) key is a lower bound of the
-// ranks it holds, so the smallest over the warps of the ceil(n / warps)-th largest thread key
-// has at least n keys at or above it; the few keys not below it are gathered and ranked by
-// counting.  A second kernel, one CTA per row, merges the chunks the same way.
+// Bound by HBM: the 4 V bytes of a row are read once.  A CTA streams a chunk of one row in tiles of 16
+// logits a thread, the next tile's loads in flight meanwhile.  Every thread keeps its own (m, S, A), so
+// nothing is exchanged until the chunk's end.  The top n are found without sorting: in the first tile
+// every thread's largest (logit, id) key is a lower bound of the ranks it holds, so the smallest over
+// the warps of the ceil(n / warps)-th largest thread key has at least n keys at or above it.  From then
+// on only keys not below that bound are gathered (a comparison with the thread's maximum for most
+// threads); the gathered ones are ranked by counting at the end.  A second kernel, one CTA per row,
+// merges the chunks the same way.
 #include <algorithm>
 
 #include "common.cuh"
@@ -26,12 +28,14 @@ namespace lp {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
-constexpr int kCap = 512;  // gathered keys; more of them (rows of a special pattern) are bisected
+constexpr int kTileLogits = 16 * kThreads;
+constexpr int kCap = 1024;  // gathered keys; a tile that brings more (rising logits) is searched by bits
+constexpr int kHigh = 512;  // more than these after a tile are thinned out
 
 typedef unsigned long long u64;
 
 struct Params {
-  int rows, V, ld, top, chunks;
+  int rows, V, ld, top, chunks, chunk_logits;
   float c;     // log2(e) / T
   float invT;
   const float *z;
@@ -65,16 +69,15 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
 
 struct Select {
   u64 keys[kCap];
+  u64 best[kMaxTop];
   u64 tau[kWarps];
   int count;
 };
 
-// The n largest of the CTA's keys, handed to out(rank, key).  each(f) calls f on all keys that
-// the thread holds, `mine` is their largest.  Every thread of the CTA calls it.
-template <typename Each, typename Out>
-__device__ __forceinline__ void block_top(Select &s, int n, u64 mine, const Each &each,
-                                          const Out &out) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// A bound that at least n of the CTA's keys reach (1 where there are fewer keys): `mine` is the
+// largest key of the thread.  Every thread of the CTA calls it; it ends behind a barrier.
+__device__ __forceinline__ u64 block_bound(Select &s, int n, u64 mine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (n + kWarps - 1) / kWarps;
   u64 left = mine, top = 0;
   for (int i = 0; i < per; ++i) {
@@ -82,54 +85,59 @@ __device__ __forceinline__ void block_top(Select &s, int n, u64 mine, const Each
     if (left == top) left = 0;  // keys differ, so one lane gives up its own
   }
   if (lane == 0) s.tau[warp] = top;
-  if (tid == 0) s.count = 0;
   __syncthreads();
   u64 tau = s.tau[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) tau = min(tau, s.tau[w]);
-  if (tau == 0) tau = 1;  // 0 is no key
-  if (mine >= tau)
-    each([&](u64 k) {
-      if (k >= tau) {
-        const int at = atomicAdd(&s.count, 1);
-        if (at < kCap) s.keys[at] = k;
-      }
-    });
-  __syncthreads();
-  int count = s.count;
-  if (count > kCap) {
-    // the n-th largest key, bit by bit: the largest threshold that n keys reach
-    u64 t = 0;
-    for (int bit = 63; bit >= 0; --bit) {
-      const u64 v = t | (1ull << bit);
-      int have = 0;
-      if (mine >= v) each([&](u64 k) { have += k >= v; });
-      for (int o = 16; o > 0; o >>= 1) have += __shfl_xor_sync(0xffffffffu, have, o);
-      __syncthreads();
-      if (tid == 0) s.count = 0;
-      __syncthreads();
-      if (lane == 0) atomicAdd(&s.count, have);
-      __syncthreads();
-      if (s.count >= n) t = v;
-    }
-    __syncthreads();
-    if (tid == 0) s.count = 0;
-    __syncthreads();
-    if (t == 0) t = 1;
-    if (mine >= t)
-      each([&](u64 k) {
-        if (k >= t) s.keys[atomicAdd(&s.count, 1)] = k;  // n of them: the keys differ
-      });
-    __syncthreads();
-    count = s.count;
-  }
-  for (int i = tid; i < count; i += kThreads) {
+  return tau == 0 ? 1 : tau;  // 0 is no key
+}
+
+// The n largest of s.keys[0 .. count) to s.best in their order (0 behind the last key).  Callers have
+// a barrier before and after.
+__device__ __forceinline__ void block_rank(Select &s, int n, int count) {
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (i >= count) s.best[i] = 0;
+  for (int i = threadIdx.x; i < count; i += kThreads) {
     const u64 k = s.keys[i];
     int rank = 0;
     for (int j = 0; j < count; ++j) rank += s.keys[j] > k;
-    if (rank < n) out(rank, k);
+    if (rank < n) s.best[rank] = k;
   }
-  for (int i = count + tid; i < n; i += kThreads) out(i, (u64)0);  // fewer than n keys at all
+}
+
+// Keeps the n largest of s.keys[0 .. count); returns the smallest of them (or 1).
+__device__ __noinline__ u64 block_thin(Select &s, int n, int count) {
+  u64 mine = 0;
+  for (int i = threadIdx.x; i < count; i += kThreads) mine = s.keys[i] > mine ? s.keys[i] : mine;
+  const u64 bound = block_bound(s, n, mine);
+  u64 held[kCap / kThreads];
+#pragma unroll
+  for (int i = 0; i < kCap / kThreads; ++i) {
+    const int at = threadIdx.x + i * kThreads;
+    held[i] = at < count ? s.keys[at] : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.count = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kCap / kThreads; ++i)
+    if (held[i] >= bound) s.keys[atomicAdd(&s.count, 1)] = held[i];
+  __syncthreads();
+  const int left = s.count;
+  block_rank(s, n, left);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kThreads) s.keys[i] = s.best[i];
+  if (threadIdx.x == 0) s.count = min(n, left);
+  const u64 last = s.best[n - 1];
+  __syncthreads();
+  return last == 0 ? 1 : last;
+}
+
+// One key more of a thread (0: none) where it reaches the bound; barriers around it are the caller's.
+__device__ __forceinline__ void gather(Select &s, u64 k, u64 bound) {
+  if (k < bound) return;
+  const int at = atomicAdd(&s.count, 1);
+  if (at < kCap) s.keys[at] = k;
 }
 
 __device__ __forceinline__ float block_max(float v, float *red) {
@@ -162,6 +170,7 @@ __device__ __forceinline__ void block_sum2(float &a, float &b, float *red) {
 }
 
 constexpr float kLowest = -1e4f;  // 2^kLowest is 0, and 0 * kLowest is 0
+constexpr float kFloor = -3.402823466e38f;  // maximum of no logits: -inf minus it is -inf, not NaN
 
 // Answers of one row from its (m, S, A); bad rows get NaN.
 __device__ __forceinline__ void answer(const Params &p, int row, int token, float m, float S,
@@ -198,93 +207,139 @@ __device__ __forceinline__ bool scored(const Params &p, int row, int &token, boo
   return false;
 }
 
-// One chunk of one row.  EPT logits a thread, in float4 quads where VEC (rows 16-byte aligned).
-// With one chunk a row the kernel writes the answers itself.
-template <int EPT, bool VEC>
-__global__ void __launch_bounds__(kThreads) chunk_kernel(const __grid_constant__ Params p) {
+// Sixteen logits of a thread; element e has id base + tile_id(e).
+template <bool VEC>
+__device__ __forceinline__ int tile_id(int e) {
+  return VEC ? (e / 4) * (4 * kThreads) + 4 * (int)threadIdx.x + e % 4
+             : e * kThreads + (int)threadIdx.x;
+}
+template <bool VEC>
+__device__ __forceinline__ void load_tile(const float *z, int base, int V, float (&x)[16]) {
+  if (base + kTileLogits <= V) {
+#pragma unroll
+    for (int e = 0; e < 16; e += VEC ? 4 : 1) {
+      if constexpr (VEC) {
+        const float4 f = __ldcs(reinterpret_cast<const float4 *>(z + base + tile_id<VEC>(e)));
+        x[e] = f.x, x[e + 1] = f.y, x[e + 2] = f.z, x[e + 3] = f.w;
+      } else {
+        x[e] = __ldcs(z + base + tile_id<VEC>(e));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int v = base + tile_id<VEC>(e);
+      x[e] = v < V ? __ldcs(z + v) : -INFINITY;
+    }
+  }
+}
+
+// One chunk of one row, in float4 quads where VEC (rows 16-byte aligned).  With one chunk a row the
+// kernel writes the answers itself.
+template <bool VEC, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constant__ Params p) {
   __shared__ Select sel;
   __shared__ float red[3 * kWarps];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x;
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const float *z = p.z + (size_t)row * p.ld;
+  const int begin = chunk * p.chunk_logits, end = min(p.V, begin + p.chunk_logits);
+  float x[16];
+  load_tile<VEC>(z, begin, end, x);  // before the token: a row that is not scored is read in vain
   int token;
   if (!scored(p, row, token, p.chunks == 1)) return;
-  const float *z = p.z + (size_t)row * p.ld;
-  const int base = chunk * (kThreads * EPT);
-  float x[EPT];
-  // element e of the thread has id base + id_of(e)
-  auto id_of = [&](int e) {
-    return VEC ? (e / 4) * (4 * kThreads) + 4 * tid + e % 4 : e * kThreads + tid;
-  };
-  if constexpr (VEC) {
+  if (TOP && tid == 0) sel.count = 0;
+  float m = kFloor, S = 0.f, A = 0.f;
+  u64 bound = 0;         // keys below it are not gathered
+  float bound_z = 0.f;   // its logit
+  for (int base = begin; base < end; base += kTileLogits) {
+    float next[16];
+    if (base + kTileLogits < end) load_tile<VEC>(z, base + kTileLogits, end, next);
+    float mt = x[0];
 #pragma unroll
-    for (int q = 0; q < EPT / 4; ++q) {
-      const int v = base + q * 4 * kThreads + 4 * tid;
-      if (v + 3 < p.V) {
-        const float4 f = __ldcs(reinterpret_cast<const float4 *>(z + v));
-        x[4 * q] = f.x, x[4 * q + 1] = f.y, x[4 * q + 2] = f.z, x[4 * q + 3] = f.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[4 * q + e] = v + e < p.V ? z[v + e] : -INFINITY;
-      }
+    for (int e = 1; e < 16; ++e) mt = fmaxf(mt, x[e]);
+    if (mt > m) {
+      const float d = fmaxf((m - mt) * p.c, kLowest), w = ex2_approx(d);
+      A = S > 0.f ? w * fmaf(d, S, A) : 0.f;
+      S *= w;
+      m = mt;
     }
-  } else {
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const int v = base + e * kThreads + tid;
-      x[e] = v < p.V ? __ldcs(z + v) : -INFINITY;
-    }
-  }
-  float m = -INFINITY;
-  bool odd = false;  // NaN or +inf
-  int arg = 0;       // element of the thread's largest key: the first of its largest logit
-#pragma unroll
-  for (int e = 0; e < EPT; ++e) {
-    odd |= !(x[e] < INFINITY);
-    if (x[e] > m) {
-      m = x[e];
-      arg = e;
-    }
-  }
-  odd = __syncthreads_or(odd);
-  const float M = block_max(m, red);
-  float S = 0.f, A = 0.f;
-  if (!odd && M > -INFINITY) {
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-      const float t = fmaxf((x[e] - M) * p.c, kLowest);
+    for (int e = 0; e < 16; ++e) {
+      const float t = (x[e] - m) * p.c;  // NaN or +inf: S becomes NaN
       const float w = ex2_approx(t);
       S += w;
-      A = fmaf(w, t, A);
+      A = fmaf(w, fmaxf(t, kLowest), A);
     }
+    if (TOP) {
+      if (base == begin) {
+        u64 mine = 0;
+#pragma unroll
+        for (int e = 15; e >= 0; --e)
+          if (x[e] == mt && base + tile_id<VEC>(e) < end) mine = key_of(mt, base + tile_id<VEC>(e));
+        bound = block_bound(sel, p.top, mine);
+        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
+      }
+      const int before = sel.count;  // the last write is behind a barrier
+      __syncthreads();
+      if (mt >= bound_z) {
+        uint32_t mask = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mask |= x[e] >= bound_z ? 1u << e : 0u;
+        for (; mask; mask &= mask - 1) {  // few: their logits are read again
+          const int v = base + tile_id<VEC>(__ffs(mask) - 1);
+          if (v < end) gather(sel, key_of(z[v], v), bound);
+        }
+      }
+      __syncthreads();
+      int count = sel.count;
+      if (__builtin_expect(count > kCap, 0)) {
+        // more than there is room for: 256 keys at a time, thinned out in between
+        __syncthreads();
+        if (tid == 0) sel.count = before;
+        for (int e = 0; e < 16; ++e) {
+          __syncthreads();
+          const int v = base + tile_id<VEC>(e);
+          if (v < end) gather(sel, key_of(z[v], v), bound);
+          __syncthreads();
+          count = sel.count;
+          if (count > kHigh) {
+            bound = block_thin(sel, p.top, count);
+            count = p.top;
+          }
+        }
+        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
+      }
+      // the first tile's bound is a loose one
+      if (__builtin_expect(count > (base == begin ? 2 * p.top : kHigh), 0)) {
+        bound = block_thin(sel, p.top, count);
+        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = next[e];
   }
+  const float M = block_max(m, red);
+  const float d = fmaxf((m - M) * p.c, kLowest), w = ex2_approx(d);
+  A = S > 0.f ? w * fmaf(d, S, A) : 0.f;
+  S *= w;
   block_sum2(S, A, red + kWarps);
   const bool one = p.chunks == 1;
-  const bool bad = odd || S == 0.f;
+  const bool bad = !(S > 0.f) || !(S < INFINITY);
   if (tid == 0) {
-    if (one)
-      answer(p, row, token, M, S, A, bad);
-    else
-      p.part[blockIdx.x] = make_float4(odd ? __int_as_float(0x7fc00000) : M, S, A, 0.f);
+    if (one) answer(p, row, token, M, S, A, bad);
+    else p.part[blockIdx.x] = make_float4(M, S, A, 0.f);
   }
-  if (p.top == 0) return;
+  if (!TOP) return;
+  block_thin(sel, p.top, sel.count);
   const float lnS = logf(S);
-  // a thread whose first element lies behind the row's end holds no key
-  const u64 mine = base + id_of(arg) < p.V ? key_of(m, base + id_of(arg)) : 0;
-  block_top(
-      sel, p.top, odd ? 0 : mine,
-      [&](auto f) {
-#pragma unroll
-        for (int e = 0; e < EPT; ++e)
-          if (base + id_of(e) < p.V) f(key_of(x[e], base + id_of(e)));
-      },
-      [&](int rank, u64 k) {
-        if (one)
-          answer_top(p, row, rank, k, M, lnS, bad || k == 0);
-        else
-          p.cand[(size_t)blockIdx.x * p.top + rank] = k;
-      });
+  if (tid < p.top) {
+    const u64 k = sel.best[tid];
+    if (one) answer_top(p, row, tid, k, M, lnS, bad || k == 0);
+    else p.cand[(size_t)blockIdx.x * p.top + tid] = k;
+  }
 }
 
 // Merges the chunks of one row.
@@ -293,62 +348,80 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
   __shared__ float red[3 * kWarps];
   pdl_wait();
   const int tid = threadIdx.x, row = blockIdx.x;
-  int token;
-  if (!scored(p, row, token, true)) return;
   const float4 *part = p.part + (size_t)row * p.chunks;
-  float m = -INFINITY;
-  bool odd = false;
-  for (int i = tid; i < p.chunks; i += kThreads) {
-    const float v = part[i].x;
-    odd |= v != v;
-    m = fmaxf(m, v);
-  }
-  odd = __syncthreads_or(odd);
-  const float M = block_max(m, red);
-  float S = 0.f, A = 0.f;
-  if (!odd && M > -INFINITY)
-    for (int i = tid; i < p.chunks; i += kThreads) {
-      const float4 v = part[i];
-      const float d = fmaxf((v.x - M) * p.c, kLowest);
-      const float w = ex2_approx(d);
-      S = fmaf(v.y, w, S);
-      A = fmaf(w, fmaf(d, v.y, v.z), A);
-    }
-  block_sum2(S, A, red + kWarps);
-  const bool bad = odd || S == 0.f;
-  if (tid == 0) answer(p, row, token, M, S, A, bad);
-  if (p.top == 0) return;
-  const float lnS = logf(S);
   const u64 *cand = p.cand + (size_t)row * p.chunks * p.top;
   const int n = p.chunks * p.top;
+  // the first values of each kind are requested together
+  const float4 first = tid < p.chunks ? part[tid] : make_float4(kFloor, 0.f, 0.f, 0.f);
+  u64 held[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) held[i] = tid + i * kThreads < n ? cand[tid + i * kThreads] : 0;
+  int token;
+  if (!scored(p, row, token, true)) return;
+  if (tid == 0) sel.count = 0;
+  float m = first.x;
+  for (int i = tid + kThreads; i < p.chunks; i += kThreads) m = fmaxf(m, part[i].x);
+  const float M = block_max(m, red);
+  float S = 0.f, A = 0.f;
+  for (int i = tid; i < p.chunks; i += kThreads) {
+    const float4 v = i == tid ? first : part[i];
+    const float d = fmaxf((v.x - M) * p.c, kLowest);
+    const float w = ex2_approx(d);
+    S = fmaf(v.y, w, S);
+    A = fmaf(w, fmaf(d, v.y, v.z), A);
+  }
+  block_sum2(S, A, red + kWarps);
+  const bool bad = !(S > 0.f) || !(S < INFINITY);
+  if (tid == 0) answer(p, row, token, M, S, A, bad);
+  if (p.top == 0) return;
   auto each = [&](auto f) {
-    for (int i = tid; i < n; i += kThreads) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (held[i]) f(held[i]);
+    for (int i = tid + 4 * kThreads; i < n; i += kThreads) {
       const u64 k = cand[i];
       if (k) f(k);
     }
   };
   u64 mine = 0;
-  if (!odd) each([&](u64 k) { mine = k > mine ? k : mine; });
-  block_top(sel, p.top, mine, each, [&](int rank, u64 k) {
-    answer_top(p, row, rank, k, M, lnS, bad || k == 0);
-  });
+  each([&](u64 k) { mine = k > mine ? k : mine; });
+  u64 bound = block_bound(sel, p.top, mine);
+  each([&](u64 k) { gather(sel, k, bound); });
+  __syncthreads();
+  if (sel.count > kCap) {
+    __syncthreads();
+    if (tid == 0) sel.count = 0;
+    for (int i = 0; i < n; i += kThreads) {
+      __syncthreads();
+      if (i + tid < n) gather(sel, cand[i + tid], bound);
+      __syncthreads();
+      const int count = sel.count;
+      if (count > kHigh) bound = block_thin(sel, p.top, count);
+    }
+    __syncthreads();
+  }
+  block_rank(sel, p.top, sel.count);
+  __syncthreads();
+  const float lnS = logf(S);
+  if (tid < p.top) answer_top(p, row, tid, sel.best[tid], M, lnS, bad || sel.best[tid] == 0);
 }
 
 // ------------------------------------------------------------------------------- host side
 
 struct Split {
-  int ept, chunks;
+  int chunk_logits, chunks;
 };
 
-// 8192 logits a CTA, fewer while that leaves SMs idle (one row of 262144: 32 CTAs; with 2048
-// logits each, 128).
+// Chunks of whole tiles, as long as they still give four CTAs an SM (one tile at least, and at most
+// what keeps the row's candidates few).
 static Split split(const sd_logprobs_desc *d) {
-  const long long sms = std::max(sm_count(), 1);
-  Split s{32, 0};
-  for (;; s.ept /= 2) {
-    s.chunks = (int)(((long long)d->vocab + kThreads * s.ept - 1) / (kThreads * s.ept));
-    if (s.ept == 8 || (long long)s.chunks * d->rows >= sms) return s;
-  }
+  const long long ctas = 4ll * std::max(sm_count(), 1);
+  const long long tiles = ((long long)d->vocab + kTileLogits - 1) / kTileLogits;
+  const long long per = std::min(std::max(tiles * d->rows / ctas, 1ll), 16ll);
+  Split s;
+  s.chunk_logits = (int)(per * kTileLogits);
+  s.chunks = (int)((tiles + per - 1) / per);
+  return s;
 }
 
 static sd_status validate(const sd_logprobs_desc *d) {
@@ -402,6 +475,7 @@ sd_status sd_logprobs(const sd_logprobs_desc *desc, const float *logits, const i
   p.ld = desc->ld_logits ? desc->ld_logits : desc->vocab;
   p.top = desc->top_n;
   p.chunks = s.chunks;
+  p.chunk_logits = s.chunk_logits;
   p.invT = 1.f / desc->temperature;
   p.c = 1.4426950408889634f / desc->temperature;
   p.z = logits;
@@ -419,15 +493,12 @@ sd_status sd_logprobs(const sd_logprobs_desc *desc, const float *logits, const i
   const dim3 grid((unsigned)(p.rows * p.chunks)), block(kThreads);
   const cudaStream_t cs = (cudaStream_t)stream;
   cudaError_t e;
-  if (s.ept == 32)
-    e = vec ? launch(chunk_kernel<32, true>, grid, block, 0, cs, p)
-            : launch(chunk_kernel<32, false>, grid, block, 0, cs, p);
-  else if (s.ept == 16)
-    e = vec ? launch(chunk_kernel<16, true>, grid, block, 0, cs, p)
-            : launch(chunk_kernel<16, false>, grid, block, 0, cs, p);
+  if (p.top > 0)
+    e = vec ? launch(chunk_kernel<true, true>, grid, block, 0, cs, p)
+            : launch(chunk_kernel<false, true>, grid, block, 0, cs, p);
   else
-    e = vec ? launch(chunk_kernel<8, true>, grid, block, 0, cs, p)
-            : launch(chunk_kernel<8, false>, grid, block, 0, cs, p);
+    e = vec ? launch(chunk_kernel<true, false>, grid, block, 0, cs, p)
+            : launch(chunk_kernel<false, false>, grid, block, 0, cs, p);
   if (e != cudaSuccess) return SD_ERR_CUDA;
   if (p.chunks == 1) return SD_OK;
   return cuda_status(launch(merge_kernel, dim3((unsigned)p.rows), block, 0, cs, p));

@@ -11,12 +11,11 @@
 //
 // Bound by HBM: the 4 V bytes of a row are read once.  A CTA streams a chunk of one row in tiles of 16
 // logits a thread, the next tile's loads in flight meanwhile.  Every thread keeps its own (m, S, A), so
-// nothing is exchanged until the chunk's end.  The top n are found without sorting: in the first tile
-// every thread's largest (logit, id) key is a lower bound of the ranks it holds, so the smallest over
-// the warps of the ceil(n / warps)-th largest thread key has at least n keys at or above it.  From then
-// on only keys not below that bound are gathered (a comparison with the thread's maximum for most
-// threads); the gathered ones are ranked by counting at the end.  A second kernel, one CTA per row,
-// merges the chunks the same way.
+// nothing is exchanged until the chunk's end.  The top n are found without sorting: the n-th largest of
+// the first tile's thread maxima (of at most 8 a warp) is a logit that at least n reach.  Only logits
+// that reach the bound are gathered as (logit, id) keys, a comparison with the thread's maximum for most
+// threads; where many are, they are ranked by counting and the n-th becomes the bound.  A second
+// kernel, one CTA per row, merges the chunks' sums and ranks their keys.
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,6 +30,7 @@ constexpr int kMaxTop = 32;
 constexpr int kTileLogits = 16 * kThreads;
 constexpr int kCap = 1024;  // gathered keys; a tile that brings more (rising logits) is searched by bits
 constexpr int kHigh = 512;  // more than these after a tile are thinned out
+constexpr int kDump = 64;   // keys that a chunk leaves for the merge, in any order
 
 typedef unsigned long long u64;
 
@@ -43,7 +43,7 @@ struct Params {
   float *logprob, *entropy, *top_lp;
   int32_t *top_ids;
   float4 *part;  // [rows][chunks] (m, S, A, -)
-  u64 *cand;     // [rows][chunks][top]
+  u64 *cand;     // [rows][chunks][kDump]
   int *status;
 };
 
@@ -59,37 +59,45 @@ __device__ __forceinline__ float key_logit(u64 k) {
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-__device__ __forceinline__ u64 warp_max(u64 v) {
-  for (int o = 16; o > 0; o >>= 1) {
-    const u64 u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 struct Select {
   u64 keys[kCap];
   u64 best[kMaxTop];
-  u64 tau[kWarps];
+  float tau[8 * kWarps];
+  float bound;
   int count;
 };
 
-// A bound that at least n of the CTA's keys reach (1 where there are fewer keys): `mine` is the
-// largest key of the thread.  Every thread of the CTA calls it; it ends behind a barrier.
-__device__ __forceinline__ u64 block_bound(Select &s, int n, u64 mine) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per = (n + kWarps - 1) / kWarps;
-  u64 left = mine, top = 0;
+// A logit that at least n of the CTA's logits reach (-inf where there are fewer): the n-th largest of the
+// warps' min(n, 8) largest thread maxima.  `mine` is the thread's largest.  Every thread of the CTA
+// calls it; it ends behind a barrier.
+__device__ __forceinline__ float block_bound(Select &s, int n, float mine) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = min(n, 8);
+  float left = mine, kept = -INFINITY;
+#pragma unroll 1
   for (int i = 0; i < per; ++i) {
-    top = warp_max(left);
-    if (left == top) left = 0;  // keys differ, so one lane gives up its own
+    const float top = warp_max(left);
+    const unsigned who = __ballot_sync(0xffffffffu, left == top);
+    if (lane == __ffs(who) - 1) left = -INFINITY;
+    if (lane == i) kept = top;
   }
-  if (lane == 0) s.tau[warp] = top;
+  if (lane < per) s.tau[warp * per + lane] = kept == kept ? kept : -INFINITY;
+  if (tid == 0) s.bound = -INFINITY;
   __syncthreads();
-  u64 tau = s.tau[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) tau = min(tau, s.tau[w]);
-  return tau == 0 ? 1 : tau;  // 0 is no key
+  if (tid < kWarps * per) {
+    const float v = s.tau[tid];
+    int rank = 0;
+    for (int i = 0; i < kWarps * per; ++i) rank += s.tau[i] > v || (s.tau[i] == v && i < tid);
+    if (rank == n - 1) s.bound = v;
+  }
+  __syncthreads();
+  return s.bound;
 }
 
 // The n largest of s.keys[0 .. count) to s.best in their order (0 behind the last key).  Callers have
@@ -105,23 +113,22 @@ __device__ __forceinline__ void block_rank(Select &s, int n, int count) {
   }
 }
 
-// Keeps the n largest of s.keys[0 .. count); returns the smallest of them (or 1).
+// Keeps the n largest of s.keys[0 .. count), sorted in s.best too; returns the smallest of them (or 1).
 __device__ __noinline__ u64 block_thin(Select &s, int n, int count) {
-  u64 mine = 0;
-  for (int i = threadIdx.x; i < count; i += kThreads) mine = s.keys[i] > mine ? s.keys[i] : mine;
-  const u64 bound = block_bound(s, n, mine);
+  float mine = -INFINITY;
   u64 held[kCap / kThreads];
 #pragma unroll
   for (int i = 0; i < kCap / kThreads; ++i) {
     const int at = threadIdx.x + i * kThreads;
     held[i] = at < count ? s.keys[at] : 0;
+    if (held[i]) mine = fmaxf(mine, key_logit(held[i]));
   }
-  __syncthreads();
+  const float bound = block_bound(s, n, mine);
   if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kCap / kThreads; ++i)
-    if (held[i] >= bound) s.keys[atomicAdd(&s.count, 1)] = held[i];
+    if (held[i] && key_logit(held[i]) >= bound) s.keys[atomicAdd(&s.count, 1)] = held[i];
   __syncthreads();
   const int left = s.count;
   block_rank(s, n, left);
@@ -252,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constan
   if (!scored(p, row, token, p.chunks == 1)) return;
   if (TOP && tid == 0) sel.count = 0;
   float m = kFloor, S = 0.f, A = 0.f;
-  u64 bound = 0;         // keys below it are not gathered
-  float bound_z = 0.f;   // its logit
+  u64 bound = 1;        // keys below it are not gathered,
+  float bound_z = 0.f;  // nor logits below it
   for (int base = begin; base < end; base += kTileLogits) {
     float next[16];
     if (base + kTileLogits < end) load_tile<VEC>(z, base + kTileLogits, end, next);
@@ -274,14 +281,7 @@ __global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constan
       A = fmaf(w, fmaxf(t, kLowest), A);
     }
     if (TOP) {
-      if (base == begin) {
-        u64 mine = 0;
-#pragma unroll
-        for (int e = 15; e >= 0; --e)
-          if (x[e] == mt && base + tile_id<VEC>(e) < end) mine = key_of(mt, base + tile_id<VEC>(e));
-        bound = block_bound(sel, p.top, mine);
-        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
-      }
+      if (base == begin) bound_z = block_bound(sel, p.top, mt);
       const int before = sel.count;  // the last write is behind a barrier
       __syncthreads();
       if (mt >= bound_z) {
@@ -310,12 +310,13 @@ __global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constan
             count = p.top;
           }
         }
-        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
+        if (bound > 1) bound_z = key_logit(bound);
       }
-      // the first tile's bound is a loose one
-      if (__builtin_expect(count > (base == begin ? 2 * p.top : kHigh), 0)) {
+      // A higher bound spares later tiles the gathering (every gathered key stalls its warp for a
+      // read): ranking at 4 n keys rather than at 512 took 192 rows from 54 to 50 us.
+      if (__builtin_expect(count > max(kDump, 4 * p.top), 0) && base + kTileLogits < end) {
         bound = block_thin(sel, p.top, count);
-        bound_z = bound > 1 ? key_logit(bound) : -INFINITY;
+        if (bound > 1) bound_z = key_logit(bound);
       }
     }
 #pragma unroll
@@ -333,29 +334,30 @@ __global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constan
     else p.part[blockIdx.x] = make_float4(M, S, A, 0.f);
   }
   if (!TOP) return;
-  block_thin(sel, p.top, sel.count);
-  const float lnS = logf(S);
-  if (tid < p.top) {
-    const u64 k = sel.best[tid];
-    if (one) answer_top(p, row, tid, k, M, lnS, bad || k == 0);
-    else p.cand[(size_t)blockIdx.x * p.top + tid] = k;
+  const int count = sel.count;
+  if (one || count > kDump) block_thin(sel, p.top, count);
+  if (!one) {
+    if (tid < kDump) p.cand[(size_t)blockIdx.x * kDump + tid] = tid < sel.count ? sel.keys[tid] : 0;
+  } else if (tid < p.top) {
+    answer_top(p, row, tid, sel.best[tid], M, logf(S), bad || sel.best[tid] == 0);
   }
 }
 
 // Merges the chunks of one row.
+constexpr int kHeld = 6;  // candidates a thread requests with its first loads (24 chunks)
 __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__ Params p) {
   __shared__ Select sel;
   __shared__ float red[3 * kWarps];
   pdl_wait();
   const int tid = threadIdx.x, row = blockIdx.x;
   const float4 *part = p.part + (size_t)row * p.chunks;
-  const u64 *cand = p.cand + (size_t)row * p.chunks * p.top;
-  const int n = p.chunks * p.top;
+  const u64 *cand = p.cand + (size_t)row * p.chunks * kDump;
+  const int n = p.top > 0 ? p.chunks * kDump : 0;
   // the first values of each kind are requested together
   const float4 first = tid < p.chunks ? part[tid] : make_float4(kFloor, 0.f, 0.f, 0.f);
-  u64 held[4];
+  u64 held[kHeld];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) held[i] = tid + i * kThreads < n ? cand[tid + i * kThreads] : 0;
+  for (int i = 0; i < kHeld; ++i) held[i] = tid + i * kThreads < n ? cand[tid + i * kThreads] : 0;
   int token;
   if (!scored(p, row, token, true)) return;
   if (tid == 0) sel.count = 0;
@@ -376,27 +378,30 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(const __grid_constant__
   if (p.top == 0) return;
   auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kHeld; ++i)
       if (held[i]) f(held[i]);
-    for (int i = tid + 4 * kThreads; i < n; i += kThreads) {
+    for (int i = tid + kHeld * kThreads; i < n; i += kThreads) {
       const u64 k = cand[i];
       if (k) f(k);
     }
   };
-  u64 mine = 0;
-  each([&](u64 k) { mine = k > mine ? k : mine; });
-  u64 bound = block_bound(sel, p.top, mine);
-  each([&](u64 k) { gather(sel, k, bound); });
+  float mine = -INFINITY;
+  each([&](u64 k) { mine = fmaxf(mine, key_logit(k)); });
+  const float bound = block_bound(sel, p.top, mine);
+  each([&](u64 k) {
+    if (key_logit(k) >= bound) gather(sel, k, 1);
+  });
   __syncthreads();
   if (sel.count > kCap) {
     __syncthreads();
     if (tid == 0) sel.count = 0;
+    u64 least = 1;
     for (int i = 0; i < n; i += kThreads) {
       __syncthreads();
-      if (i + tid < n) gather(sel, cand[i + tid], bound);
+      if (i + tid < n) gather(sel, cand[i + tid], least);
       __syncthreads();
       const int count = sel.count;
-      if (count > kHigh) bound = block_thin(sel, p.top, count);
+      if (count > kHigh) least = block_thin(sel, p.top, count);
     }
     __syncthreads();
   }
@@ -412,12 +417,13 @@ struct Split {
   int chunk_logits, chunks;
 };
 
-// Chunks of whole tiles, as long as they still give four CTAs an SM (one tile at least, and at most
-// what keeps the row's candidates few).
+// Chunks of whole tiles: as many a row as give one wave of four CTAs an SM (192 rows of 262144: 3 of 22
+// tiles), and no longer than 24 tiles, so that more rows than CTAs still spread evenly.
 static Split split(const sd_logprobs_desc *d) {
   const long long ctas = 4ll * std::max(sm_count(), 1);
   const long long tiles = ((long long)d->vocab + kTileLogits - 1) / kTileLogits;
-  const long long per = std::min(std::max(tiles * d->rows / ctas, 1ll), 16ll);
+  const long long want = std::min(std::max(ctas / std::max(d->rows, 1), 1ll), tiles);
+  const long long per = std::min((tiles + want - 1) / want, 24ll);
   Split s;
   s.chunk_logits = (int)(per * kTileLogits);
   s.chunks = (int)((tiles + per - 1) / per);
@@ -451,7 +457,8 @@ size_t sd_logprobs_workspace_size(const sd_logprobs_desc *desc) {
   if (validate(desc) != SD_OK || desc->rows == 0) return 0;
   const Split s = split(desc);
   if (s.chunks == 1) return 0;
-  return part_bytes(desc, s) + (size_t)desc->rows * s.chunks * desc->top_n * sizeof(u64);
+  return part_bytes(desc, s) +
+         (desc->top_n > 0 ? (size_t)desc->rows * s.chunks * kDump * sizeof(u64) : 0);
 }
 
 sd_status sd_logprobs(const sd_logprobs_desc *desc, const float *logits, const int32_t *tokens,

@@ -17,7 +17,9 @@
 // that unit of several heads.  Bound by HBM: every element is read and written once.
 //
 // The append to an e4m3 cache: a CTA owns one (block, heads, K or V), so the block's scale has
-// one writer.  The rows stay in registers between the maximum and the rounding.
+// one writer.  It goes from head to head, the next head's rows in flight while this one's maximum
+// is joined; a thread has the same elements of every head and keeps their sines and cosines in
+// shared memory.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -31,7 +33,6 @@ namespace sdv {
 namespace app {
 
 constexpr int kMaxThreads = 256;
-constexpr int kHeadsAtOnce = 4;  // heads whose loads a thread issues together
 
 struct Rot {
   const unsigned long long *freqs;  // null: no rotation
@@ -66,7 +67,7 @@ struct Params {
   int64_t ld_k, ld_v;
   uint8_t *kc, *vc;
   float *ks, *vs;
-  int items, chunks, quant_ctas;
+  int items, chunks, heads_per_quant, quant_ctas;
   int *status;
 };
 
@@ -223,9 +224,9 @@ __device__ __forceinline__ void row_place(const Params &p, int row, bool cache, 
 }
 
 // Rows [rows_per_cta * cta, ...) of head group hg: each thread one unit of one row, the heads of
-// the group in runs of kHeadsAtOnce.
-template <typename T, int V>
-__device__ void rows_body(const Params &p, int cta, int hg) {
+// the group in runs of HEADS whose loads are issued together.
+template <typename T, int V, int HEADS>
+__device__ __forceinline__ void rows_body(const Params &p, int cta, int hg) {
   __shared__ int s_pos[kMaxThreads];
   __shared__ long long s_slot[kMaxThreads];
   const int tid = threadIdx.x;
@@ -248,12 +249,12 @@ __device__ void rows_body(const Params &p, int cta, int hg) {
     const Unit un = unit_of<V>(p, u);
     float c[V], s[V];
     bool have = false;
-    for (int h = h0; h < h1; h += kHeadsAtOnce) {
-      Vec<T, V> v0[kHeadsAtOnce], v1[kHeadsAtOnce];
-      T *dst[kHeadsAtOnce];
-      bool rot[kHeadsAtOnce];
+    for (int h = h0; h < h1; h += HEADS) {
+      Vec<T, V> v0[HEADS], v1[HEADS];
+      T *dst[HEADS];
+      bool rot[HEADS];
 #pragma unroll
-      for (int e = 0; e < kHeadsAtOnce; ++e) {
+      for (int e = 0; e < HEADS; ++e) {
         dst[e] = nullptr;
         rot[e] = false;
         int g = h + e;
@@ -277,7 +278,7 @@ __device__ void rows_body(const Params &p, int cta, int hg) {
         have = true;
       }
 #pragma unroll
-      for (int e = 0; e < kHeadsAtOnce; ++e) {
+      for (int e = 0; e < HEADS; ++e) {
         if (dst[e] == nullptr) continue;
         if (rot[e]) {
           float a[V], b[V];
@@ -298,7 +299,7 @@ template <typename T, int V>
 __global__ void __launch_bounds__(kMaxThreads) rows_kernel(const __grid_constant__ Params p) {
   pdl_trigger();
   pdl_wait();
-  rows_body<T, V>(p, blockIdx.x, blockIdx.y);
+  rows_body<T, V, 4>(p, blockIdx.x, blockIdx.y);
 }
 
 // ------------------------------------------------------------------------- e4m3 append
@@ -334,9 +335,10 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const float (&x)[V], f
 }
 
 // Largest finite magnitude; what is not finite does not count.
+constexpr float kFinite = 3.402823466e38f;
 __device__ __forceinline__ float amax_of(float m, float x) {
   const float a = fabsf(x);
-  return a <= 3.402823466e38f ? fmaxf(m, a) : m;
+  return a <= kFinite ? fmaxf(m, a) : m;
 }
 
 // Item t: the t-th slot of the blocks that receive rows.  Sequence b has the slots from
@@ -358,16 +360,22 @@ __device__ __forceinline__ int seq_of_item(const Params &p, int t, int &first) {
   return lo;
 }
 
-// One CTA: the rows that one call adds to one cache block, for HC heads of K or V.
-// U units of each head stay in the thread's registers from the maximum to the rounding; U == 0
-// reads the rows a second time instead (blocks of more than 8 * 256 units).
-template <typename T, int V, int U, int HC>
-__device__ void quant_body(const Params &p, int cta) {
+constexpr int kMaxHeads = 8;  // heads of a CTA
+
+// One CTA: the rows that one call adds to one cache block, for up to heads_per_quant heads of K or
+// V.  U units of a head stay in the thread's registers from the maximum to the rounding; U == 0
+// (more than 2 units a thread) goes over the rows twice.
+template <typename T, int V, int U>
+__device__ __forceinline__ void quant_body(const Params &p, int cta) {
+  constexpr int Q = V / 4;  // float4 quads of a unit's cosines
+  constexpr int UR = U > 0 ? U : 1;
+  __shared__ float4 s_cos[UR * Q * kMaxThreads], s_sin[UR * Q * kMaxThreads];
+  __shared__ unsigned s_max[2][kMaxThreads / 32];
+  __shared__ float s_old[kMaxHeads];
   const int per_item = 2 * p.chunks;
   const int item = cta / per_item, part = cta % per_item;
   const bool is_v = part >= p.chunks;
-  const int h0 = (is_v ? part - p.chunks : part) * HC;
-  __shared__ float s_max[kMaxThreads / 32][HC];
+  const int h0 = (is_v ? part - p.chunks : part) * p.heads_per_quant;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   int b, i, row0, n;
@@ -405,110 +413,107 @@ __device__ void quant_body(const Params &p, int cta) {
     return;
   }
   const int rows = (int)(end - at_ll), off = (int)(at_ll % p.bs);
-  const T *src = reinterpret_cast<const T *>(is_v ? p.v_new : p.k_new) +
-                 (row0 + (long long)(at - L)) * (is_v ? p.ld_v : p.ld_k);
   const int64_t ld = is_v ? p.ld_v : p.ld_k;
+  const T *src = reinterpret_cast<const T *>(is_v ? p.v_new : p.k_new) +
+                 (row0 + (long long)(at - L)) * ld + (long long)h0 * p.D;
   uint8_t *codes = (is_v ? p.vc : p.kc) + ((size_t)blk * p.hkv + h0) * p.bs * p.D;
   float *scale = (is_v ? p.vs : p.ks) + (size_t)blk * p.hkv + h0;
-  const int heads = min(HC, p.hkv - h0);
+  const int heads = min(p.heads_per_quant, p.hkv - h0);
   const bool rot = !is_v && p.rot.freqs != nullptr;
-  const int total = rows * p.units;
 
-  constexpr int UR = U > 0 ? U : 1;
-  constexpr bool kKeepTurns = U == 1 || U == 2;  // 2 V registers a unit
-  Vec<T, V> v0[UR][HC], v1[UR][HC];
-  float c[kKeepTurns ? UR : 1][V], s[kKeepTurns ? UR : 1][V];
-  float m[HC];
-#pragma unroll
-  for (int h = 0; h < HC; ++h) m[h] = 0.f;
-
-  auto load = [&](int w, int k) {
-    const int r = w / p.units;
-    const Unit un = unit_of<V>(p, w - r * p.units);
-#pragma unroll
-    for (int h = 0; h < HC; ++h)
-      if (h < heads) {
-        const T *x = src + r * ld + (long long)(h0 + h) * p.D;
-        v0[k][h] = *reinterpret_cast<const Vec<T, V> *>(x + un.p0);
-        if (un.two) v1[k][h] = *reinterpret_cast<const Vec<T, V> *>(x + un.p1);
-      }
+  // place of unit w: source and destination of head 0, distance of its second vector (0: none)
+  struct Place {
+    const T *src;
+    uint8_t *dst;
+    int second;
+    bool rot;
   };
-  auto turns = [&](int w, int k) {
+  // w's place; its cosines and sines go to slot k of the thread
+  auto place = [&](int w, int k) {
     const int r = w / p.units, u = w - r * p.units;
-    if (rot && u < p.nrot) unit_turns<V>(p, u, at + r, c[k], s[k]);
+    const Unit un = unit_of<V>(p, u);
+    Place x;
+    x.src = src + r * ld + un.p0;
+    x.dst = codes + (size_t)(off + r) * p.D + un.p0;
+    x.second = un.two ? un.p1 - un.p0 : 0;
+    x.rot = rot && un.rot;
+    if (x.rot) {
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        float c[4], s[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          turn(p.rot.freqs[u * V + 4 * q + e], at + r, p.rot.amp, c[e], s[e]);
+        const int to = (k * Q + q) * kMaxThreads + tid;
+        s_cos[to] = make_float4(c[0], c[1], c[2], c[3]);
+        s_sin[to] = make_float4(s[0], s[1], s[2], s[3]);
+      }
+    }
+    return x;
   };
-  // the unit's values of one head, turned
-  auto values = [&](int w, int k, int kt, int h, float (&a)[V], float (&bb)[V]) {
-    const int r = w / p.units;
-    const Unit un = unit_of<V>(p, w - r * p.units);
-    v0[k][h].get(a);
-    if (un.two) {
-      v1[k][h].get(bb);
+  auto load = [&](const Place &x, int h, Vec<T, V> &v0, Vec<T, V> &v1) {
+    const T *y = x.src + h * p.D;
+    v0 = *reinterpret_cast<const Vec<T, V> *>(y);
+    if (x.second) v1 = *reinterpret_cast<const Vec<T, V> *>(y + x.second);
+  };
+  // the unit's values, turned
+  auto values = [&](const Place &x, int k, const Vec<T, V> &v0, const Vec<T, V> &v1, float (&a)[V],
+                    float (&bb)[V]) {
+    v0.get(a);
+    if (x.second) {
+      v1.get(bb);
     } else {
 #pragma unroll
       for (int e = 0; e < V; ++e) bb[e] = 0.f;
     }
-    if (rot && un.rot) unit_rotate<V>(p.rot.inter, c[kt], s[kt], a, bb);
-  };
-  auto take_max = [&](int w, int k, int kt) {
+    if (x.rot) {
+      float c[V], s[V];
 #pragma unroll
-    for (int h = 0; h < HC; ++h)
-      if (h < heads) {
-        float a[V], bb[V];
-        values(w, k, kt, h, a, bb);
-#pragma unroll
-        for (int e = 0; e < V; ++e) m[h] = amax_of(amax_of(m[h], a[e]), bb[e]);
+      for (int q = 0; q < Q; ++q) {
+        const float4 y = s_cos[(k * Q + q) * kMaxThreads + tid];
+        const float4 z = s_sin[(k * Q + q) * kMaxThreads + tid];
+        c[4 * q] = y.x, c[4 * q + 1] = y.y, c[4 * q + 2] = y.z, c[4 * q + 3] = y.w;
+        s[4 * q] = z.x, s[4 * q + 1] = z.y, s[4 * q + 2] = z.z, s[4 * q + 3] = z.w;
       }
+      unit_rotate<V>(p.rot.inter, c, s, a, bb);
+    }
   };
-
-  if constexpr (U > 0) {
+  // largest finite magnitude: the plain maximum, and again with care where an infinity is in it
+  auto largest = [&](const float (&a)[V], const float (&bb)[V]) {
+    float mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (tid + k * (int)blockDim.x < total) load(tid + k * blockDim.x, k);
+    for (int e = 0; e < V; ++e) mx = fmaxf(mx, fmaxf(fabsf(a[e]), fabsf(bb[e])));
+    if (__builtin_expect(mx > kFinite, 0)) {
+      mx = 0.f;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int w = tid + k * blockDim.x;
-      if (w < total) {
-        turns(w, kKeepTurns ? k : 0);
-        take_max(w, k, kKeepTurns ? k : 0);
-      }
+      for (int e = 0; e < V; ++e) mx = amax_of(amax_of(mx, a[e]), bb[e]);
     }
-  } else {
-    for (int w = tid; w < total; w += blockDim.x) {
-      load(w, 0);
-      turns(w, 0);
-      take_max(w, 0, 0);
-    }
-  }
-#pragma unroll
-  for (int h = 0; h < HC; ++h)
-    for (int o = 16; o > 0; o >>= 1) m[h] = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], o));
-  if (lane == 0) {
-#pragma unroll
-    for (int h = 0; h < HC; ++h) s_max[warp][h] = m[h];
-  }
-  // scales of a block that goes on; a block is begun by the call that writes its first row
-  float old[HC];
-#pragma unroll
-  for (int h = 0; h < HC; ++h) old[h] = off > 0 && h < heads ? scale[h] : 0.f;
-  __syncthreads();
-  float inv[HC];
-  const int warps = (blockDim.x + 31) >> 5;
-#pragma unroll
-  for (int h = 0; h < HC; ++h) {
-    if (h >= heads) continue;
-    float mx = s_max[0][h];
-    for (int q = 1; q < warps; ++q) mx = fmaxf(mx, s_max[q][h]);
-    float sc = pow2i(scale_exp(mx));
+    return mx;
+  };
+  auto put = [&](const Place &x, int h, float inv, const float (&a)[V], const float (&bb)[V]) {
+    uint8_t *y = x.dst + (size_t)h * p.bs * p.D;
+    store_codes<V>(y, a, inv);
+    if (x.second) store_codes<V>(y + x.second, bb, inv);
+  };
+  // The scale of head h from the threads' maxima; ends with its inverse.
+  auto join = [&](int h, float m) {
+    // floats that are not negative rise with their bits
+    const unsigned mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == 0) s_max[h & 1][warp] = mw;
+    __syncthreads();
+    const unsigned mine = lane < ((int)blockDim.x + 31) >> 5 ? s_max[h & 1][lane] : 0u;
+    m = __uint_as_float(__reduce_max_sync(0xffffffffu, mine));
+    float sc = pow2i(scale_exp(m));
+    const float old = s_old[h];
     if (off > 0) {
-      if (!(old[h] > 0.f && old[h] < INFINITY)) {
+      if (!(old > 0.f && old < INFINITY)) {
         if (tid == 0) record_status(p.status, SD_ERR_DEVICE);
-      } else if (old[h] >= sc) {
-        sc = old[h];
+      } else if (old >= sc) {
+        sc = old;
       } else {
         // the block's live rows move to the larger scale: a power of two, so only codes that
         // become subnormal are rounded again
-        const float f = old[h] / sc;
+        const float f = old / sc;
         uint8_t *x = codes + (size_t)h * p.bs * p.D;
         for (int w = tid; w < off * p.D / 4; w += blockDim.x) {
           const uint32_t q = reinterpret_cast<const uint32_t *>(x)[w];
@@ -524,52 +529,72 @@ __device__ void quant_body(const Params &p, int cta) {
         }
       }
     }
-    inv[h] = 1.f / sc;  // exact: sc is a power of two
-    // old[] was read before the barrier by every thread, so the new scale may be written now
-    if (tid == 0) scale[h] = sc;
-  }
-  auto put = [&](int w, int k, int kt) {
-    const int r = w / p.units;
-    const Unit un = unit_of<V>(p, w - r * p.units);
-#pragma unroll
-    for (int h = 0; h < HC; ++h)
-      if (h < heads) {
-        float a[V], bb[V];
-        values(w, k, kt, h, a, bb);
-        uint8_t *x = codes + ((size_t)h * p.bs + off + r) * p.D;
-        store_codes<V>(x + un.p0, a, inv[h]);
-        if (un.two) store_codes<V>(x + un.p1, bb, inv[h]);
-      }
+    if (tid == 0) scale[h] = sc;  // read by all before the first barrier
+    return 1.f / sc;              // exact: sc is a power of two
   };
+
+  // a block is begun by the call that writes its first row
+  if (tid < heads) s_old[tid] = off > 0 ? scale[tid] : 0.f;
+  const int total = rows * p.units;
   if constexpr (U > 0) {
+    Place x[U];
+    Vec<T, V> v0[U], v1[U];
+    const int mine = total - tid;  // unit k is this thread's if k blockDim < mine
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int w = tid + k * blockDim.x;
-      if (w < total) {
-        if (!kKeepTurns) turns(w, 0);
-        put(w, k, kKeepTurns ? k : 0);
+    for (int k = 0; k < U; ++k)
+      if (k * (int)blockDim.x < mine) {
+        x[k] = place(tid + k * blockDim.x, k);
+        load(x[k], 0, v0[k], v1[k]);
       }
+    __syncthreads();
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h) {
+      float a[U][V], bb[U][V], m = 0.f;
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (k * (int)blockDim.x < mine) {
+          values(x[k], k, v0[k], v1[k], a[k], bb[k]);
+          m = fmaxf(m, largest(a[k], bb[k]));
+          if (h + 1 < heads) load(x[k], h + 1, v0[k], v1[k]);
+        }
+      const float inv = join(h, m);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (k * (int)blockDim.x < mine) put(x[k], h, inv, a[k], bb[k]);
     }
   } else {
-    for (int w = tid; w < total; w += blockDim.x) {
-      load(w, 0);
-      turns(w, 0);
-      put(w, 0, 0);
+    __syncthreads();
+#pragma unroll 1
+    for (int h = 0; h < heads; ++h) {
+      float m = 0.f, inv = 0.f;
+#pragma unroll 1
+      for (int step = 0; step < 2; ++step) {
+        if (step == 1) inv = join(h, m);
+        for (int w = tid; w < total; w += blockDim.x) {
+          const Place x = place(w, 0);
+          Vec<T, V> v0, v1;
+          float a[V], bb[V];
+          load(x, h, v0, v1);
+          values(x, 0, v0, v1, a, bb);
+          if (step == 0) m = fmaxf(m, largest(a, bb));
+          else put(x, h, inv, a, bb);
+        }
+      }
     }
   }
 }
 
 // The first quant_ctas CTAs quantise K and V; the others turn the query rows.
-template <typename T, int V, int U, int HC>
-__global__ void __launch_bounds__(kMaxThreads) quant_kernel(const __grid_constant__ Params p) {
+template <typename T, int V, int U>
+__global__ void __launch_bounds__(kMaxThreads, 3) quant_kernel(const __grid_constant__ Params p) {
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < p.quant_ctas) {
-    quant_body<T, V, U, HC>(p, blockIdx.x);
+    quant_body<T, V, U>(p, blockIdx.x);
   } else {
     const int groups = (p.heads_total + p.heads_per_cta - 1) / p.heads_per_cta;
     const int q = blockIdx.x - p.quant_ctas;
-    rows_body<T, V>(p, q / groups, q % groups);
+    rows_body<T, V, 2>(p, q / groups, q % groups);
   }
 }
 
@@ -641,19 +666,19 @@ static sd_status launch_rows_typed(Params &p, sd_dtype dt, bool vec, cudaStream_
   return vec ? launch_rows<float, 4>(p, st) : launch_rows<float, 1>(p, st);
 }
 
-// Registers hold the rows of a block up to 8 units a thread; four heads at a time (their turns
-// are computed once) unless that leaves SMs idle or the registers do not suffice.
+// A CTA takes up to eight heads of K or V (they share the table of sines), fewer where that leaves
+// SMs idle.
 template <typename T, int V>
 static sd_status launch_quant(Params &p, int max_rows, cudaStream_t st) {
   set_units(p, V);
-  const int units = max_rows * p.units;
-  int threads = std::min(kMaxThreads, (units + 31) / 32 * 32);
-  int U = (units + threads - 1) / threads;
-  U = U <= 1 ? 1 : U <= 2 ? 2 : U <= 4 ? 4 : U <= 8 ? 8 : 0;
+  const long long units = (long long)max_rows * p.units;
+  int threads = (int)std::min<long long>(kMaxThreads, (units + 31) / 32 * 32);
   const int sms = std::max(sm_count(), 1);
-  const bool four = U == 1 || U == 2 ? (long long)p.items * 2 * ((p.hkv + 3) / 4) >= 2 * sms : false;
-  const int HC = four ? 4 : 1;
-  p.chunks = (p.hkv + HC - 1) / HC;
+  int per = std::min(p.hkv, kMaxHeads);
+  while (per > 1 && (long long)p.items * 2 * ((p.hkv + per - 1) / per) < 2 * sms)
+    per = (per + 1) / 2;
+  p.heads_per_quant = per;
+  p.chunks = (p.hkv + per - 1) / per;
   const long long quant = (long long)p.items * 2 * p.chunks;
   long long extra = 0;
   if (p.seg[0].heads > 0) {
@@ -667,13 +692,10 @@ static sd_status launch_quant(Params &p, int max_rows, cudaStream_t st) {
   if (quant + extra > 0x7fffffffll) return SD_ERR_UNSUPPORTED;
   p.quant_ctas = (int)quant;
   const dim3 grid((unsigned)(quant + extra)), block(threads);
-  cudaError_t e;
-#define SDV_CASE(UU, HH) \
-  if (U == UU && HC == HH) e = launch(quant_kernel<T, V, UU, HH>, grid, block, 0, st, p); else
-  SDV_CASE(1, 1) SDV_CASE(2, 1) SDV_CASE(4, 1) SDV_CASE(8, 1) SDV_CASE(0, 1) SDV_CASE(1, 4)
-  SDV_CASE(2, 4) return SD_ERR_UNSUPPORTED;
-#undef SDV_CASE
-  return cuda_status(e);
+  if (units <= threads) return cuda_status(launch(quant_kernel<T, V, 1>, grid, block, 0, st, p));
+  if (units <= 2 * threads)
+    return cuda_status(launch(quant_kernel<T, V, 2>, grid, block, 0, st, p));
+  return cuda_status(launch(quant_kernel<T, V, 0>, grid, block, 0, st, p));
 }
 
 static Rot make_rot(const sd_rotary *r) {

@@ -16,10 +16,13 @@
 // row, V rotating pairs (two 16-byte vectors), computes its V sines and cosines once and turns
 // that unit of several heads.  Bound by HBM: every element is read and written once.
 //
-// The append to an e4m3 cache: a CTA owns one (block, heads, K or V), so the block's scale has
-// one writer.  It goes from head to head, the next head's rows in flight while this one's maximum
-// is joined; a thread has the same elements of every head and keeps their sines and cosines in
-// shared memory.
+// The append to an e4m3 cache: a CTA owns one (block, heads, K or V), so the block's scale has one
+// writer.  It goes from head to head, the next head's rows in flight while this one's maximum is
+// joined; a thread has the same elements of every head and keeps their sines and cosines in shared
+// memory.  Bound by issue slots and latency, not by HBM: 57.7 us for 190 MB (3.3 TB/s, blocks of 16
+// rows, 4 heads of 512 elements), 48 without a rotation; leaving out the stores alone changed nothing.
+// Staging a block's rows in shared memory and going over them twice took 61 us, with copies a block
+// ahead 59, and with loops in place of unrolled heads 81.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -32,7 +35,8 @@
 namespace sdv {
 namespace app {
 
-constexpr int kMaxThreads = 256;
+constexpr int kMaxThreads = 256;    // rows_kernel
+constexpr int kQuantThreads = 512;  // quant_kernel
 
 struct Rot {
   const unsigned long long *freqs;  // null: no rotation
@@ -316,10 +320,15 @@ __device__ __forceinline__ float pow2i(int e) {  // -126 <= e <= 127
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Two floats to two e4m3 bytes, nearest even, beyond the range to +-448, NaN to NaN.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Four floats to e4m3 bytes, nearest even, beyond the range to +-448, NaN to NaN.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
 
@@ -328,8 +337,7 @@ __device__ __forceinline__ void store_codes(uint8_t *dst, const float (&x)[V], f
   uint32_t w[V / 4];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i)
-    w[i] = e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-           e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16;
+    w[i] = e4m3x4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
   if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
   else *reinterpret_cast<uint32_t *>(dst) = w[0];
 }
@@ -360,24 +368,14 @@ __device__ __forceinline__ int seq_of_item(const Params &p, int t, int &first) {
   return lo;
 }
 
-constexpr int kMaxHeads = 8;  // heads of a CTA
+// What one call adds to one cache block: rows of a sequence from source row `row` on, to the block's
+// rows from off on.
+struct Piece {
+  int row, at, rows, off, blk;  // at: position of the first row; rows 0: nothing to do
+};
 
-// One CTA: the rows that one call adds to one cache block, for up to heads_per_quant heads of K or
-// V.  U units of a head stay in the thread's registers from the maximum to the rounding; U == 0
-// (more than 2 units a thread) goes over the rows twice.
-template <typename T, int V, int U>
-__device__ __forceinline__ void quant_body(const Params &p, int cta) {
-  constexpr int Q = V / 4;  // float4 quads of a unit's cosines
-  constexpr int UR = U > 0 ? U : 1;
-  __shared__ float4 s_cos[UR * Q * kMaxThreads], s_sin[UR * Q * kMaxThreads];
-  __shared__ unsigned s_max[2][kMaxThreads / 32];
-  __shared__ float s_old[kMaxHeads];
-  const int per_item = 2 * p.chunks;
-  const int item = cta / per_item, part = cta % per_item;
-  const bool is_v = part >= p.chunks;
-  const int h0 = (is_v ? part - p.chunks : part) * p.heads_per_quant;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-
+__device__ __forceinline__ Piece piece_of(const Params &p, int item) {
+  Piece x{};
   int b, i, row0, n;
   if (p.cu == nullptr) {
     const int per = (p.per_seq + p.bs - 2) / p.bs + 1;  // blocks that per_seq rows can touch
@@ -392,36 +390,63 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
     row0 = p.cu[b];
     n = p.cu[b + 1] - row0;
     if (row0 < 0 || n < 0 || row0 + n > p.rows || i < 0) {
-      if (tid == 0) record_status(p.status, SD_ERR_DEVICE);
-      return;
+      record_status(p.status, SD_ERR_DEVICE);
+      return x;
     }
   }
+  if (n == 0) return x;
   const int L = p.ctx_len[b];
-  if (n == 0) return;
   if (L < 0) {
-    if (tid == 0) record_status(p.status, SD_ERR_DEVICE);
-    return;
+    record_status(p.status, SD_ERR_DEVICE);
+    return x;
   }
+  // in the block's own rows: the call's begin at L % bs of block L / bs
+  const int l0 = L % p.bs, skip = i > 0 ? i * p.bs - l0 : 0;  // rows of the call before this block
+  if (skip >= n) return x;
   const int bi = L / p.bs + i;
-  const long long at_ll = max((long long)L, (long long)bi * p.bs);  // first new position here
-  const long long end = min((long long)L + n, ((long long)bi + 1) * p.bs);
-  if (at_ll >= end) return;
-  const int at = (int)at_ll;
-  const int blk = bi < p.mbps ? p.table[(size_t)b * p.mbps + bi] : -1;
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (tid == 0) record_status(p.status, SD_ERR_DEVICE);
-    return;
+  x.blk = bi < p.mbps ? p.table[(size_t)b * p.mbps + bi] : -1;
+  if (x.blk < 0 || x.blk >= p.num_blocks) {
+    record_status(p.status, SD_ERR_DEVICE);
+    return x;
   }
-  const int rows = (int)(end - at_ll), off = (int)(at_ll % p.bs);
+  x.off = i > 0 ? 0 : l0;
+  x.row = row0 + skip;
+  x.at = L + skip;
+  x.rows = min(n - skip, p.bs - x.off);
+  return x;
+}
+
+constexpr int kMaxHeads = 8;  // heads of a CTA
+
+// One CTA: one piece, for up to heads_per_quant heads of K or V.  U units of a head stay in the
+// thread's registers from the maximum to the rounding; U == 0 (more than 2 units a thread) goes over
+// the rows twice.
+template <typename T, int V, int U>
+__device__ __forceinline__ void quant_body(const Params &p, int cta) {
+  constexpr int Q = V / 4;  // float4 quads of a unit's cosines
+  extern __shared__ float4 s_turns[];  // [unit of the thread][cosines, sines][Q][thread]
+  __shared__ unsigned s_max[2][kQuantThreads / 32];
+  __shared__ unsigned s_most[kMaxHeads];
+  __shared__ float s_old[kMaxHeads];
+  const int per_item = 2 * p.chunks;
+  const int item = cta / per_item, part = cta % per_item;
+  const bool is_v = part >= p.chunks;
+  const int h0 = (is_v ? part - p.chunks : part) * p.heads_per_quant;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+
+  const Piece pc = piece_of(p, item);
+  const int rows = pc.rows, off = pc.off, at = pc.at;
+  if (rows == 0) return;
   const int64_t ld = is_v ? p.ld_v : p.ld_k;
   const T *src = reinterpret_cast<const T *>(is_v ? p.v_new : p.k_new) +
-                 (row0 + (long long)(at - L)) * ld + (long long)h0 * p.D;
-  uint8_t *codes = (is_v ? p.vc : p.kc) + ((size_t)blk * p.hkv + h0) * p.bs * p.D;
-  float *scale = (is_v ? p.vs : p.ks) + (size_t)blk * p.hkv + h0;
+                 pc.row * ld + (long long)h0 * p.D;
+  uint8_t *codes = (is_v ? p.vc : p.kc) + ((size_t)pc.blk * p.hkv + h0) * p.bs * p.D;
+  float *scale = (is_v ? p.vs : p.ks) + (size_t)pc.blk * p.hkv + h0;
   const int heads = min(p.heads_per_quant, p.hkv - h0);
   const bool rot = !is_v && p.rot.freqs != nullptr;
 
-  // place of unit w: source and destination of head 0, distance of its second vector (0: none)
+  const int lg = 31 - __clz(p.units);  // head sizes make units a power of two
+  // place of unit w: source and destination of head 0, distance of its second vector
   struct Place {
     const T *src;
     uint8_t *dst;
@@ -430,12 +455,12 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
   };
   // w's place; its cosines and sines go to slot k of the thread
   auto place = [&](int w, int k) {
-    const int r = w / p.units, u = w - r * p.units;
+    const int r = w >> lg, u = w & (p.units - 1);
     const Unit un = unit_of<V>(p, u);
     Place x;
     x.src = src + r * ld + un.p0;
     x.dst = codes + (size_t)(off + r) * p.D + un.p0;
-    x.second = un.two ? un.p1 - un.p0 : 0;
+    x.second = un.p1 - un.p0;
     x.rot = rot && un.rot;
     if (x.rot) {
 #pragma unroll
@@ -444,9 +469,9 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           turn(p.rot.freqs[u * V + 4 * q + e], at + r, p.rot.amp, c[e], s[e]);
-        const int to = (k * Q + q) * kMaxThreads + tid;
-        s_cos[to] = make_float4(c[0], c[1], c[2], c[3]);
-        s_sin[to] = make_float4(s[0], s[1], s[2], s[3]);
+        float4 *to = s_turns + (2 * k * Q + q) * nt + tid;
+        to[0] = make_float4(c[0], c[1], c[2], c[3]);
+        to[Q * nt] = make_float4(s[0], s[1], s[2], s[3]);
       }
     }
     return x;
@@ -454,24 +479,19 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
   auto load = [&](const Place &x, int h, Vec<T, V> &v0, Vec<T, V> &v1) {
     const T *y = x.src + h * p.D;
     v0 = *reinterpret_cast<const Vec<T, V> *>(y);
-    if (x.second) v1 = *reinterpret_cast<const Vec<T, V> *>(y + x.second);
+    v1 = *reinterpret_cast<const Vec<T, V> *>(y + x.second);
   };
   // the unit's values, turned
   auto values = [&](const Place &x, int k, const Vec<T, V> &v0, const Vec<T, V> &v1, float (&a)[V],
                     float (&bb)[V]) {
     v0.get(a);
-    if (x.second) {
-      v1.get(bb);
-    } else {
-#pragma unroll
-      for (int e = 0; e < V; ++e) bb[e] = 0.f;
-    }
+    v1.get(bb);
     if (x.rot) {
       float c[V], s[V];
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
-        const float4 y = s_cos[(k * Q + q) * kMaxThreads + tid];
-        const float4 z = s_sin[(k * Q + q) * kMaxThreads + tid];
+        const float4 *from = s_turns + (2 * k * Q + q) * nt + tid;
+        const float4 y = from[0], z = from[Q * nt];
         c[4 * q] = y.x, c[4 * q + 1] = y.y, c[4 * q + 2] = y.z, c[4 * q + 3] = y.w;
         s[4 * q] = z.x, s[4 * q + 1] = z.y, s[4 * q + 2] = z.z, s[4 * q + 3] = z.w;
       }
@@ -493,16 +513,18 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
   auto put = [&](const Place &x, int h, float inv, const float (&a)[V], const float (&bb)[V]) {
     uint8_t *y = x.dst + (size_t)h * p.bs * p.D;
     store_codes<V>(y, a, inv);
-    if (x.second) store_codes<V>(y + x.second, bb, inv);
+    store_codes<V>(y + x.second, bb, inv);
   };
-  // The scale of head h from the threads' maxima; ends with its inverse.
+  // The CTA's maximum of head h; floats that are not negative rise with their bits.
   auto join = [&](int h, float m) {
-    // floats that are not negative rise with their bits
     const unsigned mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
     if (lane == 0) s_max[h & 1][warp] = mw;
     __syncthreads();
-    const unsigned mine = lane < ((int)blockDim.x + 31) >> 5 ? s_max[h & 1][lane] : 0u;
-    m = __uint_as_float(__reduce_max_sync(0xffffffffu, mine));
+    const unsigned all = lane < nt / 32 ? s_max[h & 1][lane] : 0u;
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, all));
+  };
+  // Settles the scale of head h, whose new rows have the maximum m; returns its inverse.
+  auto settle = [&](int h, float m) {
     float sc = pow2i(scale_exp(m));
     const float old = s_old[h];
     if (off > 0) {
@@ -515,7 +537,7 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
         // become subnormal are rounded again
         const float f = old / sc;
         uint8_t *x = codes + (size_t)h * p.bs * p.D;
-        for (int w = tid; w < off * p.D / 4; w += blockDim.x) {
+        for (int w = tid; w < off * p.D / 4; w += nt) {
           const uint32_t q = reinterpret_cast<const uint32_t *>(x)[w];
           float y[4];
 #pragma unroll
@@ -524,8 +546,7 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
             z.__x = (__nv_fp8_storage_t)(q >> (8 * e));
             y[e] = (float)z;
           }
-          reinterpret_cast<uint32_t *>(x)[w] =
-              e4m3x2(y[0] * f, y[1] * f) | e4m3x2(y[2] * f, y[3] * f) << 16;
+          reinterpret_cast<uint32_t *>(x)[w] = e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
         }
       }
     }
@@ -539,11 +560,11 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
   if constexpr (U > 0) {
     Place x[U];
     Vec<T, V> v0[U], v1[U];
-    const int mine = total - tid;  // unit k is this thread's if k blockDim < mine
+    const int mine = total - tid;  // unit k is this thread's if k nt < mine
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (k * (int)blockDim.x < mine) {
-        x[k] = place(tid + k * blockDim.x, k);
+      if (k * nt < mine) {
+        x[k] = place(tid + k * nt, k);
         load(x[k], 0, v0[k], v1[k]);
       }
     __syncthreads();
@@ -552,41 +573,59 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
       float a[U][V], bb[U][V], m = 0.f;
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (k * (int)blockDim.x < mine) {
+        if (k * nt < mine) {
           values(x[k], k, v0[k], v1[k], a[k], bb[k]);
           m = fmaxf(m, largest(a[k], bb[k]));
           if (h + 1 < heads) load(x[k], h + 1, v0[k], v1[k]);
         }
-      const float inv = join(h, m);
+      const float inv = settle(h, join(h, m));
 #pragma unroll
       for (int k = 0; k < U; ++k)
-        if (k * (int)blockDim.x < mine) put(x[k], h, inv, a[k], bb[k]);
+        if (k * nt < mine) put(x[k], h, inv, a[k], bb[k]);
     }
   } else {
+    if (tid < heads) s_most[tid] = 0u;
     __syncthreads();
 #pragma unroll 1
-    for (int h = 0; h < heads; ++h) {
-      float m = 0.f, inv = 0.f;
+    for (int step = 0; step < 2; ++step) {
 #pragma unroll 1
-      for (int step = 0; step < 2; ++step) {
-        if (step == 1) inv = join(h, m);
-        for (int w = tid; w < total; w += blockDim.x) {
-          const Place x = place(w, 0);
-          Vec<T, V> v0, v1;
-          float a[V], bb[V];
-          load(x, h, v0, v1);
-          values(x, 0, v0, v1, a, bb);
-          if (step == 0) m = fmaxf(m, largest(a, bb));
-          else put(x, h, inv, a, bb);
+      for (int w = tid; w - lane < total; w += nt) {  // a warp stays together
+        Place x{};
+        if (w < total) x = place(w, 0);
+#pragma unroll 1
+        for (int h = 0; h < heads; ++h) {
+          float a[V], bb[V], m = 0.f;
+          if (w < total) {
+            Vec<T, V> v0, v1;
+            load(x, h, v0, v1);
+            values(x, 0, v0, v1, a, bb);
+            if (step == 0) m = largest(a, bb);
+            else put(x, h, __uint_as_float(s_most[h]), a, bb);
+          }
+          if (step == 0) {
+            const unsigned mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            if (lane == 0) atomicMax(&s_most[h], mw);
+          }
         }
       }
+      if (step == 1) break;
+#pragma unroll 1
+      for (int h = 0; h < heads; ++h) {
+        __syncthreads();
+        const float inv = settle(h, __uint_as_float(s_most[h]));
+        __syncthreads();
+        if (tid == 0) s_most[h] = __float_as_uint(inv);  // from here on the inverse scale
+      }
+      __syncthreads();
     }
   }
 }
 
 // The first quant_ctas CTAs quantise K and V; the others turn the query rows.
+// U <= 1 leaves two CTAs of 512 threads on an SM: 57 us for the prompts that two units a thread, 256
+// threads and three CTAs took 59 for; two units a thread serve blocks of twice the size.
 template <typename T, int V, int U>
-__global__ void __launch_bounds__(kMaxThreads, 3) quant_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kQuantThreads, U <= 1 ? 2 : 1) quant_kernel(const __grid_constant__ Params p) {
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < p.quant_ctas) {
@@ -666,13 +705,23 @@ static sd_status launch_rows_typed(Params &p, sd_dtype dt, bool vec, cudaStream_
   return vec ? launch_rows<float, 4>(p, st) : launch_rows<float, 1>(p, st);
 }
 
-// A CTA takes up to eight heads of K or V (they share the table of sines), fewer where that leaves
-// SMs idle.
+template <typename T, int V, int U>
+static sd_status launch_quant_units(const Params &p, int ctas, int threads, cudaStream_t st) {
+  const int smem = std::max(U, 1) * threads * V * 8;  // 64 KB at most
+  cudaError_t e = cudaFuncSetAttribute(quant_kernel<T, V, U>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       std::max(U, 1) * kQuantThreads * V * 8);
+  if (e == cudaSuccess)
+    e = launch(quant_kernel<T, V, U>, dim3(ctas), dim3(threads), smem, st, p);
+  return cuda_status(e);
+}
+
+// A CTA takes up to eight heads of K or V (they share the turns), fewer where that leaves SMs idle.
 template <typename T, int V>
 static sd_status launch_quant(Params &p, int max_rows, cudaStream_t st) {
   set_units(p, V);
   const long long units = (long long)max_rows * p.units;
-  int threads = (int)std::min<long long>(kMaxThreads, (units + 31) / 32 * 32);
+  int threads = (int)std::min<long long>(kQuantThreads, (units + 31) / 32 * 32);
   const int sms = std::max(sm_count(), 1);
   int per = std::min(p.hkv, kMaxHeads);
   while (per > 1 && (long long)p.items * 2 * ((p.hkv + per - 1) / per) < 2 * sms)
@@ -691,11 +740,10 @@ static sd_status launch_quant(Params &p, int max_rows, cudaStream_t st) {
   }
   if (quant + extra > 0x7fffffffll) return SD_ERR_UNSUPPORTED;
   p.quant_ctas = (int)quant;
-  const dim3 grid((unsigned)(quant + extra)), block(threads);
-  if (units <= threads) return cuda_status(launch(quant_kernel<T, V, 1>, grid, block, 0, st, p));
-  if (units <= 2 * threads)
-    return cuda_status(launch(quant_kernel<T, V, 2>, grid, block, 0, st, p));
-  return cuda_status(launch(quant_kernel<T, V, 0>, grid, block, 0, st, p));
+  const int ctas = (int)(quant + extra);
+  if (units <= threads) return launch_quant_units<T, V, 1>(p, ctas, threads, st);
+  if (units <= 2 * threads) return launch_quant_units<T, V, 2>(p, ctas, threads, st);
+  return launch_quant_units<T, V, 0>(p, ctas, threads, st);
 }
 
 static Rot make_rot(const sd_rotary *r) {

@@ -4,8 +4,8 @@
 drafter projects the target's last-layer activation together with its own embedding of the last
 token, runs 4 transformer layers (3 sliding-window, 1 global) whose attention reads the target's
 KV cache, and hands its output row to its LM head; Gemma 4 MTP serving guide, section 4: the
-links form a chain.  This module only marshals arguments: every step is an ``sd_linear`` or
-``sd_draft_xattn`` call of the CUDA library (no arithmetic here).
+links form a chain.  This module only marshals arguments: every step is an ``sd_linear``, turn or
+cross-attention call of the CUDA library (no arithmetic here).
 
 Per link (B token rows, drafter width d, target width d_t):
 
@@ -22,8 +22,8 @@ from __future__ import annotations
 
 from dataclasses import dataclass
 
-from . import (SD_BF16, SD_EPI_ADD, SD_EPI_GEGLU, SD_EPI_STORE, SD_F32, LinearDesc,
-               sd_linear, sd_linear_workspace_size)
+from . import (SD_BF16, SD_EPI_ADD, SD_EPI_GEGLU, SD_EPI_STORE, SD_F32, LinearDesc, RopeDesc,
+               sd_draft_xattn, sd_draft_xattn_q8, sd_linear, sd_linear_workspace_size, sd_rope)
 
 RMS_EPS = 1e-6
 
@@ -99,13 +99,35 @@ def linear_desc(m, n, k, x_dtype, ld_x, epilogue, out_dtype, ld_out, **kw):
                       out_dtype=out_dtype, ld_out=ld_out, norm_eps=RMS_EPS, **kw)
 
 
+def cross_attention(shape: DrafterShape, caches, ctx_len, ws, q_pos=None, stream=None):
+    """The attend(i, q, o) of link: each layer's cross-attention into the target's cache.
+
+    caches[i]: dict(desc=AttnDesc with n_q = 1, k, v, table) of layer i, with rot=Rotary where the
+    cache holds turned keys (q is then turned in place) and k_scale, v_scale for k and v in
+    8 bits.  q_pos int32 [B], or None for ctx_len + desc.q_offset."""
+    def attend(i, q, o):
+        c, D = caches[i], shape.head_dims[i]
+        a, w = c["desc"], shape.h_q * D
+        if c.get("rot") is not None:
+            sd_rope(RopeDesc(rows=shape.batch, heads=shape.h_q, head_dim=D, ld_x=w, ld_out=w,
+                             dtype=SD_BF16, rows_per_seq=1, q_offset=a.q_offset), c["rot"], q,
+                    q_pos, ctx_len if q_pos is None else None, q, stream=stream)
+        if "k_scale" in c:
+            sd_draft_xattn_q8(a, q, c["k"], c["v"], c["k_scale"], c["v_scale"], c["table"],
+                              ctx_len, q_pos, o, ws, stream=stream)
+        else:
+            sd_draft_xattn(a, q, c["k"], c["v"], c["table"], ctx_len, q_pos, o, ws,
+                           stream=stream)
+    return attend
+
+
 def link(shape: DrafterShape, wts, buf, h_prev, tokens, ld_tokens, attend, token_sel=None,
          stream=None, wrap=None):
     """Issue one link on the stream.
 
     h_prev     bf16 [B, d_target] (device tensor or address)
     tokens     int32 token ids; row r reads tokens[r * ld_tokens + (token_sel[r] or 0)]
-    attend(i, q, o)  issues layer i's cross-attention from q into o (sd_draft_xattn)
+    attend(i, q, o)  issues layer i's cross-attention from q into o (see cross_attention)
     wrap(fn)   optional: runs fn, which issues one sd_linear call (e.g. between timing events)
     Results: buf["h"] (the LM head's input) and buf["h_back"] (the next link's activation)."""
     B, d, dt, F = shape.batch, shape.d, shape.d_target, shape.ff

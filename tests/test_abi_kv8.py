@@ -167,3 +167,12 @@ def test_binding_checks_row_tensors():
     with pytest.raises(ValueError):
         sd._rows_ptr(torch.zeros(4, 8), 8, 4, 8)  # not on a device
     assert sd._rows_ptr(None, 8, 4, 8) is None and sd._rows_ptr(A, 8, 4, 8) == A
+
+
+def test_a_temperature_whose_scale_overflows_is_refused(L):
+    """log2(e) / T has to be finite: at 3e-39 1 / T still is."""
+    d = sd.LogprobsDesc(rows=1, vocab=8, ld_logits=0, temperature=3e-39, top_n=0)
+    assert sd.sd_logprobs_workspace_size(d) == 0
+    assert L.sd_logprobs(ctypes.byref(d), A, A, A, None, None, None, None, 0, None) == BAD
+    d.rows, d.temperature = 0, 5e-39
+    assert L.sd_logprobs(ctypes.byref(d), A, A, A, None, None, None, None, 0, None) == sd.SD_OK

@@ -625,7 +625,8 @@ __device__ __forceinline__ void quant_body(const Params &p, int cta) {
 // U <= 1 leaves two CTAs of 512 threads on an SM: 57 us for the prompts that two units a thread, 256
 // threads and three CTAs took 59 for; two units a thread serve blocks of twice the size.
 template <typename T, int V, int U>
-__global__ void __launch_bounds__(kQuantThreads, U <= 1 ? 2 : 1) quant_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kQuantThreads, U <= 1 ? 2 : 1)
+    quant_kernel(const __grid_constant__ Params p) {
   pdl_trigger();
   pdl_wait();
   if ((int)blockIdx.x < p.quant_ctas) {
@@ -708,9 +709,10 @@ static sd_status launch_rows_typed(Params &p, sd_dtype dt, bool vec, cudaStream_
 template <typename T, int V, int U>
 static sd_status launch_quant_units(const Params &p, int ctas, int threads, cudaStream_t st) {
   const int smem = std::max(U, 1) * threads * V * 8;  // 64 KB at most
-  cudaError_t e = cudaFuncSetAttribute(quant_kernel<T, V, U>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       std::max(U, 1) * kQuantThreads * V * 8);
+  cudaError_t e = cudaSuccess;
+  if (U > 1)  // above the 48 KB that every kernel has
+    e = cudaFuncSetAttribute(quant_kernel<T, V, U>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             U * kQuantThreads * V * 8);
   if (e == cudaSuccess)
     e = launch(quant_kernel<T, V, U>, dim3(ctas), dim3(threads), smem, st, p);
   return cuda_status(e);
@@ -831,7 +833,8 @@ static sd_status run_append(const sd_append_desc *d, const sd_rotary *rot, const
   p.vs = v_scale;
   int max_rows = d->block_size;
   if (cu == nullptr) {
-    const long long items = (long long)d->batch * ((d->n_new + d->block_size - 2) / d->block_size + 1);
+    const long long per = ((long long)d->n_new + d->block_size - 2) / d->block_size + 1;
+    const long long items = d->batch * per;
     if (items > 0x7fffffffll) return SD_ERR_UNSUPPORTED;
     p.items = (int)items;
     max_rows = std::min(max_rows, d->n_new);

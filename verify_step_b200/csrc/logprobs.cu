@@ -433,7 +433,7 @@ static Split split(const sd_logprobs_desc *d) {
 static sd_status validate(const sd_logprobs_desc *d) {
   if (!d || d->rows < 0 || d->vocab < 1 || d->top_n < 0) return SD_ERR_INVALID_ARG;
   if (d->ld_logits != 0 && d->ld_logits < d->vocab) return SD_ERR_INVALID_ARG;
-  if (!(d->temperature > 0.f) || !(1.f / d->temperature <= 3.4e38f) ||
+  if (!(d->temperature > 0.f) || !(1.4426950408889634f / d->temperature <= 3.4e38f) ||
       !(d->temperature <= 3.4e38f))
     return SD_ERR_INVALID_ARG;
   if (d->top_n > d->vocab) return SD_ERR_INVALID_ARG;

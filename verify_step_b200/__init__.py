@@ -189,15 +189,13 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on a CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensor arguments must be contiguous")
-    return t.data_ptr()
+    raise ValueError("tensor arguments must be contiguous")
 
 
 def _rows_ptr(t, ld, rows, width):
@@ -219,10 +217,19 @@ def _rows_ptr(t, ld, rows, width):
     return t.data_ptr()
 
 
+_raw_stream = None  # torch's current stream as an address, without a Stream object around it
+
+
 def _stream(stream):
-    import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    global _raw_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        get, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+        device()  # initialises CUDA
+        _raw_stream = lambda: get(device())
+    return _raw_stream()
 
 
 def _nbytes(t):

@@ -492,7 +492,9 @@ sd_status sd_append_kv(const sd_append_desc *desc, const sd_rotary *rot, const v
  * (any such scales, not only powers of two).  All pointers but scales, tables and lengths
  * 16-byte aligned.
  *
- * Scores are exact products of the bf16 query and the e4m3 keys, accumulated in float32; softmax
+ * Scores are exact products of the bf16 query and the e4m3 keys, accumulated in float32 (query
+ * elements below 2^-13 of their row's largest are rounded, by at most 2^-21 of it; an infinity in
+ * a query makes its output row NaN); softmax
  * weights enter the second product as two e4m3 parts (8 bits), relative to the largest of each
  * 128 keys, and are accumulated in float32.  Key and value rows outside every query's range are
  * not read as numbers (any codes may stand there).  A NaN in a V row that some, not all queries

@@ -151,6 +151,20 @@ def test_zero_scales_and_zero_queries():
     c.check()
 
 
+def test_query_elements_of_unlike_size():
+    """Elements down to 2^-30 of their row's largest: what the split rounds, 2^-21 of the largest an
+    element, moves a score by at most scale 2^-21 max |q| sum |k| < 2^-16, which the 2^-10 of the bound
+    for scores covers."""
+    c = Case(31, [300, 17], 3, 8, 2, 128, 16)
+    g = torch.Generator().manual_seed(32)
+    c.q = (c.q.float() * torch.exp2(-30 * torch.rand(c.q.shape, generator=g))).bfloat16()
+    c.q[0, 0, 0] = 0
+    c.check()
+    c.q[0, 1, 1, 5] = math.inf
+    got = c.run()
+    assert np.isnan(got[0, 1, 1]).all() and np.isfinite(np.delete(got[0, 1], 1, axis=0)).all()
+
+
 def test_a_heavy_first_key_leaves_the_others_their_weight():
     """One key holds half of the weight, 12000 others share the rest: 4e-5 each, below the last
     step of an 8-bit weight relative to the heavy one, and all of them point one way."""

@@ -176,3 +176,22 @@ def test_a_temperature_whose_scale_overflows_is_refused(L):
     assert L.sd_logprobs(ctypes.byref(d), A, A, A, None, None, None, None, 0, None) == BAD
     d.rows, d.temperature = 0, 5e-39
     assert L.sd_logprobs(ctypes.byref(d), A, A, A, None, None, None, None, 0, None) == sd.SD_OK
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Before anything of the call runs: a call is launched on the current device."""
+    class Other:
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(sd, "_current_device", lambda: 0)
+    x = Other()
+    for call in (lambda: sd.sd_rope(sd.RopeDesc(), None, x, None, None, None),
+                 lambda: sd.sd_append_kv(sd.AppendDesc(), None, x, *[None] * 8),
+                 lambda: sd.sd_verify_attn_q8(sd.AttnDesc(), x, *[None] * 8),
+                 lambda: sd.sd_draft_xattn_q8(sd.AttnDesc(), x, *[None] * 9),
+                 lambda: sd.sd_logprobs(sd.LogprobsDesc(), x, None, None)):
+        with pytest.raises(ValueError, match="current device"):
+            call()

@@ -225,11 +225,14 @@ Q8 = [
     ([45, 130, 16, 31, 15], [3] * 5, False, 8, 2, 256, 16, 256, 0, "bf16"),
     ([14, 16384], [3, 3], False, 16, 4, 512, 16, 512, 0, "bf16"),
     ([0, 7, 100, 33], [40, 0, 25, 1], True, 4, 1, 64, 16, 32, 1, "bf16"),
-    ([3, 0, 60], [200, 64, 5], True, 0, 4, 512, 64, 256, 0, "bf16"),   # 8 units a thread
+    ([3, 0, 60], [200, 64, 5], True, 0, 4, 512, 64, 256, 0, "bf16"),   # rows read twice
     ([0, 100], [300, 100], True, 2, 3, 512, 128, 512, 1, "bf16"),      # rows read twice
     ([9, 48], [7, 7], False, 2, 8, 128, 48, 128, 0, "f32"),
-    ([0] * 40, [33] * 40, True, 1, 5, 128, 32, 0, 0, "bf16"),          # four heads a CTA, one left
+    ([0] * 40, [33] * 40, True, 1, 5, 128, 32, 0, 0, "bf16"),          # several heads a CTA
     ([1] * 40, [20] * 40, True, 0, 4, 512, 16, 512, 0, "f32"),
+    ([3] * 40, [100] * 40, True, 0, 10, 64, 32, 64, 1, "bf16"),        # 8 heads a CTA, 2 left
+    ([7] * 20, [130] * 20, True, 0, 3, 512, 64, 512, 0, "bf16"),       # read twice, 2 heads, 1 left
+    ([9] * 30, [70] * 30, True, 2, 4, 512, 32, 512, 0, "bf16"),        # two units a thread
 ]
 
 

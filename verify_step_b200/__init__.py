@@ -217,19 +217,34 @@ def _rows_ptr(t, ld, rows, width):
     return t.data_ptr()
 
 
-_raw_stream = None  # torch's current stream as an address, without a Stream object around it
+_cuda = None  # torch's calls for the current device and for its stream's address
+
+
+def _torch_cuda():
+    global _cuda
+    if _cuda is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        _cuda = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    return _cuda
+
+
+def _current_device():
+    return _torch_cuda()[0]()
+
+
+def _on_device(t):
+    """Refuses a tensor of another device than the current one, where the call would run."""
+    if (t is not None and not isinstance(t, int) and t.is_cuda
+            and t.get_device() != _current_device()):
+        raise ValueError("tensors must live on the current device")
 
 
 def _stream(stream):
-    global _raw_stream
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is None:
-        import torch
-        get, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
-        device()  # initialises CUDA
-        _raw_stream = lambda: get(device())
-    return _raw_stream()
+    device, raw_stream = _torch_cuda()
+    return raw_stream(device())
 
 
 def _nbytes(t):
@@ -318,7 +333,7 @@ def sd_linear(desc, x, w, out, table=None, tokens=None, token_sel=None, stream=N
 
 
 def sd_rope_freqs(desc, freqs, stream=None) -> float:
-    """Fills ``freqs`` (int64 [rot_dim / 2]: 64-bit fractions of a turn) and returns the amplitude."""
+    """Fills ``freqs`` (int64 [rot_dim / 2]: 64-bit fractions of a turn); returns the amplitude."""
     amp = ctypes.c_float(1.0)
     _check("sd_rope_freqs", lib().sd_rope_freqs(ctypes.byref(desc), _ptr(freqs), ctypes.byref(amp),
                                                 _stream(stream)))
@@ -337,6 +352,7 @@ def _ref(x):
 
 
 def sd_rope(desc, rot, x, pos, ctx_len, out, stream=None):
+    _on_device(x)
     width = desc.heads * desc.head_dim
     _check("sd_rope", lib().sd_rope(
         ctypes.byref(desc), _ref(rot), _rows_ptr(x, desc.ld_x, desc.rows, width), _ptr(pos),
@@ -345,6 +361,7 @@ def sd_rope(desc, rot, x, pos, ctx_len, out, stream=None):
 
 def sd_append_kv(desc, rot, k_new, v_new, q, k_cache, v_cache, k_scale, v_scale, block_table,
                  ctx_len, cu_new=None, q_out=None, stream=None):
+    _on_device(k_new)
     n, kv, w = desc.n_rows, desc.h_kv * desc.head_dim, desc.h_q * desc.head_dim
     _check("sd_append_kv", lib().sd_append_kv(
         ctypes.byref(desc), _ref(rot), _rows_ptr(k_new, desc.ld_k, n, kv),
@@ -359,6 +376,7 @@ def sd_verify_attn_q8_workspace_size(desc: AttnDesc) -> int:
 
 def sd_verify_attn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, out, ws,
                       stream=None):
+    _on_device(q)
     _check("sd_verify_attn_q8", lib().sd_verify_attn_q8(
         ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _ptr(block_table), _ptr(ctx_len), _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -370,6 +388,7 @@ def sd_draft_xattn_q8_workspace_size(desc: AttnDesc) -> int:
 
 def sd_draft_xattn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, q_pos,
                       out, ws, stream=None):
+    _on_device(q)
     _check("sd_draft_xattn_q8", lib().sd_draft_xattn_q8(
         ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
         _ptr(block_table), _ptr(ctx_len), _ptr(q_pos), _ptr(out), _ptr(ws), _nbytes(ws),
@@ -382,6 +401,7 @@ def sd_logprobs_workspace_size(desc: LogprobsDesc) -> int:
 
 def sd_logprobs(desc, logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None,
                 ws=None, stream=None):
+    _on_device(logits)
     _check("sd_logprobs", lib().sd_logprobs(
         ctypes.byref(desc), _ptr(logits), _ptr(tokens), _ptr(logprob), _ptr(entropy),
         _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws), _stream(stream)))

@@ -6,9 +6,10 @@
 //
 // Mathematics.  Key p has codes k_p, v_p and scales a_p, c_p (one per cache block and kv head).
 // Query q is split into two e4m3 parts, q = 2^e (q_hi + q_lo / 16): a bf16 has 8 significant bits,
-// an e4m3 part 4, so the split is exact from 2^-13 of the row's largest element on (smaller ones are off
-// by 2^-21 of it, half a step of the smallest low part).  So the scores s_p = scale 2^e a_p (k_p . q_hi + k_p . q_lo /
-// 16) come from exact 8-bit products in float32.  The weight of v_p is 2^t, t = s_p log2(e) +
+// an e4m3 part 4, so the split is exact from 2^-13 of the row's largest element on (smaller ones are
+// off by 2^-21 of it, half a step of the smallest low part).  So the scores
+// s_p = scale 2^e a_p (k_p . q_hi + k_p . q_lo / 16) come from exact 8-bit products in float32.  The
+// weight of v_p is 2^t, t = s_p log2(e) +
 // log2(c_p); per tile of 128 keys and query row, w = 2^(t - max t + 8) is split the same way into
 // w_hi + w_lo / 16 (relative error at most 2^-8, half a step of each part; w down to 2^-21 of the
 // tile's largest is kept).  A maximum of the tile, not a running one, keeps that range for every

@@ -1,0 +1,42 @@
+"""sd_verify_attn_q8 / sd_draft_xattn_q8 at the ends of what the header allows.  Tolerances are
+those of test_gpu_attn_q8, without its constant 1e-30 where outputs are small; a bf16 output below
+2^-126 is off by half its fixed step, 2^-134.
+"""
+import numpy as np
+import pytest
+
+from tests.gpu_util import status_ok
+from tests.test_gpu_attn_q8 import Case
+
+pytestmark = pytest.mark.gpu
+
+INT_MAX = 2 ** 31 - 1
+
+
+def held(c, got=None):
+    """Every output within the bound of its own size."""
+    got = c.run() if got is None else got
+    want, tol = c.reference()
+    tol = tol - 1e-30 + 2.0 ** -134
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - want) <= tol), float((np.abs(got - want) / tol).max())
+    assert status_ok()
+    return got
+
+
+# ------------------------------------------------------------------------------- windows
+
+@pytest.mark.parametrize("n_q", [3, 7])
+@pytest.mark.parametrize("window", [INT_MAX, INT_MAX - 1, INT_MAX - 200, 2 ** 30])
+def test_a_window_longer_than_every_sequence_hides_nothing(window, n_q):
+    c = Case(1, [300, 17, 126, 0], n_q, 4, 2, 128, 16)
+    plain = c.run()
+    c.desc.window = c.window = window
+    got = held(c)
+    assert np.array_equal(got, plain)
+
+
+@pytest.mark.parametrize("window,q_pos", [(INT_MAX, INT_MAX), (INT_MAX, 5), (INT_MAX - 99, INT_MAX),
+                                          (INT_MAX - 400, INT_MAX - 1)])
+def test_drafter_windows_and_positions_near_the_integer_limit(window, q_pos):
+    held(Case(2, [300, 90], 1, 4, 2, 256, 16, window, draft=True, q_pos=[q_pos] * 2))

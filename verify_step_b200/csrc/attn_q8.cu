@@ -898,8 +898,10 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         }
       }
       if (__builtin_expect(edge, 0)) {
-        const int a = p0 + key - (p.is_draft ? w.s.hi : w.s.t0);  // keys up to j = a ...
-        const int b = p.window > 0 ? p0 + key - w.s.t0 + p.window - 1 : INT_MAX;  // ... and from b on
+        // the key is for queries a <= j <= b; a window near 2^31 must not wrap around
+        const int a = p0 + key - (p.is_draft ? w.s.hi : w.s.t0);
+        const int rel = p0 + key - w.s.t0, far = p.window - 1;
+        const int b = p.window > 0 && rel <= INT_MAX - far ? rel + far : INT_MAX;
         const int4 j0 = *reinterpret_cast<const int4 *>(&sm.rowj[r0]);
         const int4 j1 = *reinterpret_cast<const int4 *>(&sm.rowj[r0 + 4]);
         const int j[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};

@@ -4,6 +4,7 @@ those of test_gpu_attn_q8, without its constant 1e-30 where outputs are small; a
 """
 import numpy as np
 import pytest
+import torch
 
 from tests.gpu_util import status_ok
 from tests.test_gpu_attn_q8 import Case
@@ -40,3 +41,36 @@ def test_a_window_longer_than_every_sequence_hides_nothing(window, n_q):
                                           (INT_MAX - 400, INT_MAX - 1)])
 def test_drafter_windows_and_positions_near_the_integer_limit(window, q_pos):
     held(Case(2, [300, 90], 1, 4, 2, 256, 16, window, draft=True, q_pos=[q_pos] * 2))
+
+
+# -------------------------------------------------------------------------------- scales
+
+@pytest.mark.parametrize("e", [-30, -79, -81, -100, -120, -126, -131, -140, 30, 100])
+@pytest.mark.parametrize("L,D", [([200, 40], 128), ([5000], 256)])
+def test_v_scales_of_any_size(L, D, e):
+    """The output scales with them; the second length is joined from many CTAs."""
+    c = Case(3, L, 3, 4, 1, D, 16)
+    c.vs[:] = 2.0 ** e
+    held(c)
+
+
+@pytest.mark.parametrize("L,D", [([200, 40], 128), ([5000], 512)])
+def test_v_scales_all_zero_give_zeros(L, D):
+    c = Case(4, L, 2, 4, 2, D, 16)
+    c.vs[:] = 0
+    got = c.run()
+    assert np.all(got == 0) and status_ok()
+
+
+@pytest.mark.parametrize("low,high", [(0.0, 1.0), (2.0 ** -100, 1.0), (2.0 ** -140, 2.0 ** -100),
+                                      (2.0 ** -60, 2.0 ** 60), (2.0 ** -20, 2.0 ** 110), (0.0, 2.0 ** -120)])
+@pytest.mark.parametrize("L", [[200, 40], [6000]])
+def test_v_scales_far_apart(L, low, high):
+    """The keys of a tiny scale still take their share of the softmax."""
+    c = Case(5, L, 3, 4, 1, 128, 16)
+    g = torch.Generator().manual_seed(6)
+    few = torch.rand(c.vs.shape, generator=g) < 0.1
+    c.vs[:] = torch.where(few, high, low)
+    held(c)
+    c.vs[:] = torch.where(few, low, high)
+    held(c)

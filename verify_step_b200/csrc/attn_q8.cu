@@ -14,7 +14,9 @@
 // w_hi + w_lo / 16 (relative error at most 2^-8, half a step of each part; w down to 2^-21 of the
 // tile's largest is kept).  A maximum of the tile, not a running one, keeps that range for every
 // tile however large a weight another tile holds.  Tiles join in float32 registers,
-// O <- O 2^(m - m') + O_tile 2^(max t - m'), l likewise from the unrounded w / c_p.
+// O <- O 2^(m - m') + O_tile 2^(max t - m').  The denominator l sums 2^(s_p log2(e)), without c_p, so it
+// has a maximum (a frame F) of its own, kept by thread: in the weights' frame a key of scale 0 would
+// vanish from it, and scales far apart would leave float32's range.  The output is 2^(m - F) O / l.
 //
 // Bound by HBM: 2 D bytes a key and kv head are read once; 4 G n_q D flops.  Both products have
 // the streamed operand as the tensor core's 128-row side, read from shared memory where TMA put
@@ -27,7 +29,7 @@
 // not every query attends to, one that splits the next item's queries; a softmax warpgroup for
 // every eight rows (thread = key) and one to four that join the output tiles (thread = output
 // column).  Scores run two tiles ahead of the outputs.  The flattened (sequence, kv head, tile) list is
-// split evenly over the CTAs, so lengths need not be alike; shared items leave (o, m, l) partials
+// split evenly over the CTAs, so lengths need not be alike; shared items leave (o, m, F, l) partials
 // that a second kernel joins in CTA order.
 //
 // Measured (floor at the copy rate of 6.54 TB/s): 8 sequences of 16384 keys, 4 kv heads of 512, one query
@@ -65,7 +67,7 @@ struct Params {
   const int32_t *table, *ctx_len, *q_pos;
   __nv_bfloat16 *out;
   float *ws_o;   // [slots][R * RG][D]
-  float *ws_ml;  // [slots][R * RG][2]
+  float4 *ws_ml;  // [slots][R * RG]: frame of o, frame of l, l, -
   int4 *ws_rec;  // [P] items to join
   int *status;
 };
@@ -260,9 +262,10 @@ struct Cfg {
   struct Small {
     alignas(16) float scales[kScaleRing][2][8];  // K's and V's of each box of a tile; -1: no such box
     alignas(16) float red[SG][2][4][8];
+    alignas(16) float frame[SG][4][8];    // of the warps' l at an item's end
     alignas(16) float tm[4][NR];          // tile maxima for the joining warps
     alignas(16) float beta[4 * JG][NR];   // their factors of a tile, by warp
-    float2 ml[2][NR];         // frame and l of an item
+    float2 ml[2][NR];         // frame F and l of an item
     float qs[2][NR];          // 2^e scale of the query rows
     uint32_t nan_rows[2];     // of an item
     alignas(16) int rowj[NR];             // query position of a row (row / G)
@@ -525,6 +528,13 @@ __device__ __forceinline__ uint32_t clean_v(const Params &p, const Walk &w, uint
   fence_proxy_async_smem();
   __syncwarp();
   return rows;
+}
+
+// What an output sum in frame 2^m is multiplied by, its denominator l in frame 2^f: 2^(m - f) / l, in two
+// factors that each stay in float32's range; 0 where there is no key.
+__device__ __forceinline__ float joined_scale(float m, float f, float l) {
+  const float h = ex2_approx(0.5f * (m - f));
+  return l != 0.f ? h * (h / l) : 0.f;
 }
 
 template <int D, int NR>
@@ -856,8 +866,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     const int box = key >> (31 - __clz(p.bk));
     const uint32_t s_at = tmem + C::S_COL + 2 * r0 + ((uint32_t)(wq * 32) << 16);
     bool bad = false;
-    // l of this thread's keys in the frame 2^F: F follows the maximum in steps of 2^20 and more.
-    // kNone stands for no key (or nothing but NaN) so far.
+    // l of this thread's keys in the frame 2^F: F follows the thread's largest score in steps of 2^20 and
+    // more.  kNone stands for no key (or nothing but NaN) so far.
     float l[8], F[8], qsc[8];
     uint32_t items = 0;
     const int j_first = sm.rowj[0], j_last = sm.rowj[NR - 1];
@@ -878,13 +888,13 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       const int p0 = w.pos();
       bad |= !wait_for(&sm.sc_full[ring], (i / kScaleRing) & 1, abort_flag);
       const float ks = sm.scales[ring][0][box];
-      const float vs = fmaxf(sm.scales[ring][1][box], 0x1p-80f);
       const bool edge = is_edge(p, w, j_first, j_last);
-      // the keys of a box that is not there weigh nothing
-      const float lvs = ks < 0.f ? -INFINITY : __log2f(vs), rvs = __frcp_rn(vs);
+      // scale 0: no weight; a box that is not there: zeros for keys, no V scale, no term of l either
+      const float lvs = ks < 0.f ? 0.f : __log2f(sm.scales[ring][1][box]);
+      const float none = ks < 0.f ? -INFINITY : 0.f;
       bad |= !wait_for(&sm.sfull[buf], (i / NS) & 1, abort_flag);
       tc_fence_after();
-      float t[8];
+      float s[8];  // log2 of a key's term of l; lvs more is its weight's
       {
         uint32_t v[16];
         tmem_ld16(s_at + buf * N2, v);
@@ -893,8 +903,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         warp_arrive(&sm.sempty[buf]);
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
-          const float s = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
-          t[r] = fmaf(s * ks, qsc[r], lvs);
+          const float x = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
+          s[r] = fmaf(x * ks, qsc[r], none);
         }
       }
       if (__builtin_expect(edge, 0)) {
@@ -907,10 +917,13 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         const int j[8] = {j0.x, j0.y, j0.z, j0.w, j1.x, j1.y, j1.z, j1.w};
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (j[r] < a || j[r] > b) t[r] = -INFINITY;
+          if (j[r] < a || j[r] > b) s[r] = -INFINITY;
       }
       // maxima of the tile
       {
+        float t[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) t[r] = s[r] + lvs;
         const float mx = warp_max8(t);
         if ((lane & 3) == 0) sm.red[wg][i & 1][wq][lane >> 2] = mx;
       }
@@ -927,21 +940,18 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
           tm[h + 2] = q ? fmaxf(tm[h + 2], x.z) : x.z;
           tm[h + 3] = q ? fmaxf(tm[h + 3], x.w) : x.w;
         }
-      float d[8];  // log2 of the weights' frame, 2^(maximum - 8), in units of l's
       bool grow = false;
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         tm[r] = fmaxf(tm[r], kNone);
-        d[r] = tm[r] - 8.f - F[r];
-        grow |= d[r] > 12.f;
+        grow |= s[r] - F[r] > 20.f;
       }
       if (__builtin_expect(grow, 0)) {
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-          if (d[r] > -8.f) {
-            l[r] *= ex2_approx(-8.f - d[r]);
-            F[r] = tm[r];
-            d[r] = -8.f;
+          if (s[r] - F[r] > 20.f) {
+            l[r] *= ex2_approx(F[r] - s[r]);
+            F[r] = s[r];
           }
       }
       bad |= !wait_for(&sm.pempty[i % NP], ((i / NP) & 1) ^ 1, abort_flag);
@@ -961,8 +971,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         float wt[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          wt[u] = ex2_approx(t[r + u] - (tm[r + u] - 8.f));
-          l[r + u] = fmaf(wt[u], rvs * ex2_approx(d[r + u]), l[r + u]);
+          wt[u] = ex2_approx(s[r + u] + lvs - (tm[r + u] - 8.f));
+          l[r + u] += ex2_approx(s[r + u] - F[r + u]);
         }
         split2(wt[0], wt[1], hi[r / 2], lo[r / 2]);
       }
@@ -972,18 +982,30 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       fence_proxy_async_smem();
       warp_arrive(&sm.pfull[i % NP]);
       if (__builtin_expect(w.last(), 0)) {
-        // l over the 128 keys; lane r of the warpgroup's first warp hands (F, l) of row r over
+        // l over the 128 keys, brought to one frame; lane r of the warpgroup's first warp hands (F, l) of
+        // row r over
         const int lb = (items - 1) & 1;
         bad |= !wait_for(&sm.lempty[lb], (((items - 1) >> 1) & 1) ^ 1, abort_flag);
         float (&red)[4][8] = sm.red[wg][(i & 1) ^ 1];
-        const float sum = warp_sum8(l);
-        if ((lane & 3) == 0) red[wq][lane >> 2] = sum;
-        bad = barrier_or(1 + wg, 128, bad);
-        if (wq == 0 && lane == 0)
+        float (&frame)[4][8] = sm.frame[wg];
+        const float top = warp_max8(F);  // lane l: of row l / 4
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            sm.ml[lb][r0 + r] =
-                make_float2(F[r], red[0][r] + red[1][r] + red[2][r] + red[3][r]);
+        for (int r = 0; r < 8; ++r)
+          l[r] *= ex2_approx(F[r] - __shfl_sync(0xffffffffu, top, 4 * r));
+        const float sum = warp_sum8(l);
+        if ((lane & 3) == 0) {
+          red[wq][lane >> 2] = sum;
+          frame[wq][lane >> 2] = top;
+        }
+        bad = barrier_or(1 + wg, 128, bad);
+        if (wq == 0 && lane < 8) {
+          float f = frame[0][lane], x = 0.f;
+#pragma unroll
+          for (int q = 1; q < 4; ++q) f = fmaxf(f, frame[q][lane]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) x = fmaf(red[q][lane], ex2_approx(frame[q][lane] - f), x);
+          sm.ml[lb][r0 + lane] = make_float2(f, x);
+        }
         // the next tile writes there again: not before the first warp has read it
         bad = barrier_or(1 + wg, 128, bad);
         warp_arrive(&sm.lfull[lb]);
@@ -1063,23 +1085,20 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       const int lb = (items - 1) & 1;
       ok = warp_wait(&sm.lfull[lb], ((items - 1) >> 1) & 1, abort_flag);
       if (!ok) break;
-      // l of row `lane` in this warp's frame
-      float l = 0.f;
-      if (lane < NR) {
-        const float2 x = sm.ml[lb][lane];
-        l = x.y * ex2_approx(x.x - m_run);
-      }
-      if (sm.nan_rows[lb] >> lane & 1) l = __int_as_float(0x7fc00000);
+      // frame and l of row `lane`
+      float2 fl = make_float2(kNone, 0.f);
+      if (lane < NR) fl = sm.ml[lb][lane];
+      if (sm.nan_rows[lb] >> lane & 1) fl.y = __int_as_float(0x7fc00000);
       // lane r: where row r goes and its factor
       const int jr = sm.rowj[min(lane, NR - 1)], row = row0 + lane;
       const size_t item = (size_t)w.b * p.Hkv + w.g, at = (item + cta) * (size_t)(p.R * p.RG) + row;
-      const float scale = !whole ? 1.f : l != 0.f ? 1.f / l : 0.f;  // no key: a zero row
+      const float scale = whole ? joined_scale(m_run, fl.x, fl.y) : 1.f;
       const unsigned long long to =
           whole ? (unsigned long long)(p.out + (((size_t)w.b * p.n_q + jr) * p.Hq + w.g * p.G + row -
                                                 (size_t)jr * p.G) * D)
                 : (unsigned long long)(p.ws_o + at * D);
       if (!whole && jg == 0 && wq == 0 && lane < rows)
-        *reinterpret_cast<float2 *>(p.ws_ml + at * 2) = make_float2(m_run, l);
+        p.ws_ml[at] = make_float4(m_run, fl.x, fl.y, 0.f);
       if (D >= 128 || wq < 2) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
@@ -1108,7 +1127,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
 // Joins the partials of items that several CTAs shared, in CTA order.  One CTA per (border between two
 // shares, row), 4 columns a thread; the attention kernel left a record of the item whose first border
 // it is.
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(128, 6) combine_kernel(const __grid_constant__ Params p) {
   pdl_wait();
   const int4 rec = p.ws_rec[blockIdx.x + 1];  // sequence, kv head, last share; -1: nothing here
   if (rec.z < 0) return;
@@ -1118,38 +1137,38 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
       p.out + (((size_t)b * p.n_q + row / p.G) * p.Hq + g * p.G + row % p.G) * p.D;
   const int d = threadIdx.x * 4;
   const size_t pitch = (size_t)p.R * p.RG;
-  float m = kNone, den = 0.f;
+  float m = kNone, f = kNone, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   // runs of 8 partials: their loads are on their way together
   for (int c = c0; c <= c1; c += 8) {
-    float2 ml[8];
+    float4 ml[8];
     float4 o[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int x = c + u;
       const bool held = x <= c1;
       const size_t at = ((size_t)item + x) * pitch + row;
-      ml[u] = held ? *reinterpret_cast<const float2 *>(p.ws_ml + at * 2)
-                   : make_float2(kNone, 0.f);
+      ml[u] = held ? p.ws_ml[at] : make_float4(kNone, kNone, 0.f, 0.f);
       o[u] = held && d < p.D ? __ldcg(reinterpret_cast<const float4 *>(p.ws_o + at * p.D + d))
                              : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float mx = m;
+    float mx = m, fx = f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) mx = fmaxf(mx, ml[u].x);
+    for (int u = 0; u < 8; ++u) mx = fmaxf(mx, ml[u].x), fx = fmaxf(fx, ml[u].y);
     const float a = ex2_approx(m - mx);
-    den *= a;
+    den *= ex2_approx(f - fx);
     acc.x *= a, acc.y *= a, acc.z *= a, acc.w *= a;
     m = mx;
+    f = fx;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const float f = ex2_approx(ml[u].x - mx);
-      den = fmaf(f, ml[u].y, den);
-      acc.x = fmaf(f, o[u].x, acc.x), acc.y = fmaf(f, o[u].y, acc.y);
-      acc.z = fmaf(f, o[u].z, acc.z), acc.w = fmaf(f, o[u].w, acc.w);
+      const float b = ex2_approx(ml[u].x - mx);
+      den = fmaf(ex2_approx(ml[u].y - fx), ml[u].z, den);
+      acc.x = fmaf(b, o[u].x, acc.x), acc.y = fmaf(b, o[u].y, acc.y);
+      acc.z = fmaf(b, o[u].z, acc.z), acc.w = fmaf(b, o[u].w, acc.w);
     }
   }
-  const float inv = den != 0.f ? 1.f / den : 0.f;
+  const float inv = joined_scale(m, f, den);
   if (d < p.D)
     *reinterpret_cast<uint2 *>(dst + d) =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -1216,7 +1235,7 @@ static size_t ws_o_bytes(const sd_attn_desc *d, const Rows &r) {
 static size_t ws_size(const sd_attn_desc *d) {
   const Rows r = rows_of(d->h_q / d->h_kv * d->n_q, d->head_dim);
   const size_t slots = (size_t)d->batch * d->h_kv + ctas(r);
-  return ws_o_bytes(d, r) + round_up(slots * r.R * r.RG * 8, 256) + ctas(r) * sizeof(int4);
+  return ws_o_bytes(d, r) + round_up(slots * r.R * r.RG * sizeof(float4), 256) + ctas(r) * sizeof(int4);
 }
 
 static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const void *kc,
@@ -1265,7 +1284,7 @@ static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const voi
   p.q_pos = q_pos;
   p.out = reinterpret_cast<__nv_bfloat16 *>(out);
   p.ws_o = reinterpret_cast<float *>(ws);
-  p.ws_ml = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ws) + ws_o_bytes(d, r));
+  p.ws_ml = reinterpret_cast<float4 *>(reinterpret_cast<uint8_t *>(ws) + ws_o_bytes(d, r));
   p.ws_rec = reinterpret_cast<int4 *>(
       reinterpret_cast<uint8_t *>(ws) + ws_size(d) - (size_t)p.P * sizeof(int4));
   p.status = device_status_word();

@@ -74,3 +74,22 @@ def test_v_scales_far_apart(L, low, high):
     held(c)
     c.vs[:] = torch.where(few, low, high)
     held(c)
+
+
+@pytest.mark.parametrize("eq,ek", [(-110, 104), (-100, 94), (-126, 120), (-90, 84), (60, -66),
+                                   (100, -106), (0, -6)])
+def test_queries_and_k_scales_of_any_size(eq, ek):
+    """Scores are about one, made of tiny queries and large scales or the other way round."""
+    c = Case(7, [300, 60], 3, 8, 2, 128, 16)
+    c.q = (c.q.double() * 2.0 ** eq).bfloat16()
+    c.ks[:] = 2.0 ** ek
+    held(c)
+
+
+def test_keys_of_zeros_under_large_scales():
+    """Their scores are 0, however large the query and the scale: the output is the values' mean."""
+    c = Case(13, [100, 20], 2, 4, 2, 128, 16)
+    c.q = (c.q.double() * 2.0 ** 120).bfloat16()
+    c.kc[:] = 0
+    c.ks[:] = 2.0 ** 60
+    held(c)

@@ -820,8 +820,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
             m = fmaxf(m, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
           }
           m = redux_max(m);
-          // 2^ex with m <= 256 * 2^ex, ex >= -100
-          const int ex = max((int)(__float_as_uint(m) >> 23) - 127 + 1 - 8, -100);
+          // 2^ex with m <= 256 * 2^ex; from ex = -126 on down every bf16 is a whole number of e4m3 steps
+          const int ex = max((int)(__float_as_uint(m) >> 23) - 127 + 1 - 8, -126);
           const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
           if (lane == 0) sm.qs[qb][r] = __uint_as_float((uint32_t)(127 + ex) << 23);
           const int n = 16 * (r >> 3) + (r & 7);
@@ -904,7 +904,8 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
 #pragma unroll
         for (int r = 0; r < 8; ++r) {
           const float x = fmaf(__uint_as_float(v[8 + r]), 0.0625f, __uint_as_float(v[r]));
-          s[r] = fmaf(x * ks, qsc[r], none);
+          // the two scales first: a tiny and a large one meet before the sum leaves float32's range
+          s[r] = fmaf(x, fminf(ks * qsc[r], 3.402823466e38f), none);
         }
       }
       if (__builtin_expect(edge, 0)) {

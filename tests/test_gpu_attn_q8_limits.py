@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import verify_step_b200 as sd
 from tests.gpu_util import status_ok
 from tests.test_gpu_attn_q8 import Case
 
@@ -93,3 +94,16 @@ def test_keys_of_zeros_under_large_scales():
     c.kc[:] = 0
     c.ks[:] = 2.0 ** 60
     held(c)
+
+
+# ------------------------------------------------------------------------------- lengths
+
+@pytest.mark.parametrize("L", [INT_MAX, INT_MAX - 1, INT_MAX - 130])
+def test_a_length_near_the_integer_limit_is_recorded(L):
+    c = Case(9, [40, 40], 3, 4, 2, 64, 16)
+    want, tol = c.reference()
+    c.L[0] = L
+    got = c.run()
+    assert sd.sd_device_status_read() == sd.SD_ERR_DEVICE
+    sd.sd_device_status_clear()
+    assert np.all(got[0] == 0) and np.all(np.abs(got - want)[1] <= tol[1])

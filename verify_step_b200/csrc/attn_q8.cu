@@ -58,6 +58,7 @@ struct Params {
   int B, n_q, Hq, Hkv, G, D, bs, mbps, num_blocks, window, M;
   int is_draft, q_offset;
   int bk, box_bytes;  // keys and bytes of one TMA box
+  int span;           // positions of a table's row, short of 2^31 by a tile and a query's rows
   int row_groups;     // 8-row groups of a cache
   int R, RG;          // row groups of an item, rows of a group
   int P;              // CTAs of one row group
@@ -85,13 +86,15 @@ __device__ __forceinline__ Seq seq_of(const Params &p, int b, bool report) {
     if (report) record_status(p.status, SD_ERR_DEVICE);
     return s;
   }
-  const int hi = p.is_draft ? min(s.t0, L - 1) : L + p.n_q - 1;
+  const int last = p.is_draft ? min(s.t0, L - 1) : L;  // the verify rows' own keys follow it
+  const int more = p.is_draft ? 0 : p.n_q - 1;
   const int lo = p.window > 0 ? max(0, s.t0 - p.window + 1) : 0;
-  if (hi < lo) return s;
-  if ((long long)hi >= (long long)p.mbps * p.bs) {
+  if (p.is_draft && last < lo) return s;
+  if (last >= p.span - more) {
     if (report) record_status(p.status, SD_ERR_DEVICE);
     return s;
   }
+  const int hi = last + more;
   s.lo = lo;
   s.hi = hi;
   s.p0 = lo / p.bk * p.bk;
@@ -1275,6 +1278,7 @@ static sd_status run(const sd_attn_desc *d, bool draft, const void *q, const voi
   // CTAs 14.3 us, on 148 14.8
   const long long span = (long long)p.mbps * p.bs;
   const long long keys = p.window ? std::min(span, (long long)p.window + p.n_q + p.bk - 2) : span;
+  p.span = (int)std::min<long long>(span, INT_MAX - kTile - 64);
   p.P = (int)std::min<long long>(ctas(r), (long long)p.B * p.Hkv * ((keys - 1) / kTile + 1));
   p.scale_log2 = d->scale * 1.4426950408889634f;
   p.q = reinterpret_cast<const __nv_bfloat16 *>(q);

@@ -431,8 +431,8 @@ sd_status sd_rope(const sd_rope_desc *desc, const sd_rotary *rot, const void *x,
  *
  * Sequence b adds n_b rows, at positions ctx_len[b] .. ctx_len[b] + n_b - 1: rows b * n_new + j
  * of k_new, v_new and q with n_b = n_new (cu_new == NULL), or rows cu_new[b] .. cu_new[b+1] - 1
- * (prompts of different lengths packed one after another; n_b may be 0; rows from
- * cu_new[batch] on are not read).  ctx_len is not advanced.
+ * (prompts of different lengths packed one after another; n_b may be 0; rows before cu_new[0]
+ * and from cu_new[batch] on are not read, their q_out rows not written).  ctx_len is not advanced.
  *   k_new, v_new [n_rows, ld], h_kv * head_dim elements of a row;  q [n_rows, ld_q] and
  *   q_out [n_rows, ld_q_out], h_q * head_dim elements (h_q == 0: none; in place allowed)
  *   k_cache, v_cache [num_blocks, h_kv, block_size, head_dim] of cache_dtype

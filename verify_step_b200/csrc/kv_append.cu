@@ -419,10 +419,11 @@ __device__ __forceinline__ Piece piece_of(const Params &p, int item) {
     i = item - first;
     row0 = p.cu[b];
     n = p.cu[b + 1] - row0;
-    if (row0 < 0 || n < 0 || row0 + n > p.rows || i < 0) {
+    if (row0 < 0 || n < 0 || row0 + n > p.rows) {
       record_status(p.status, SD_ERR_DEVICE);
       return x;
     }
+    if (i < 0) return x;  // a slot before the first sequence's: cu[0] >= bs
   }
   if (n == 0) return x;
   const int L = p.ctx_len[b];

@@ -434,7 +434,8 @@ sd_status sd_rope(const sd_rope_desc *desc, const sd_rotary *rot, const void *x,
  * (prompts of different lengths packed one after another; n_b may be 0; rows before cu_new[0]
  * and from cu_new[batch] on are not read, their q_out rows not written).  ctx_len is not advanced.
  *   k_new, v_new [n_rows, ld], h_kv * head_dim elements of a row;  q [n_rows, ld_q] and
- *   q_out [n_rows, ld_q_out], h_q * head_dim elements (h_q == 0: none; in place allowed)
+ *   q_out [n_rows, ld_q_out], h_q * head_dim elements (h_q == 0: none; in place allowed,
+ *   q_out == q with ld_q_out == ld_q; otherwise the two must not overlap)
  *   k_cache, v_cache [num_blocks, h_kv, block_size, head_dim] of cache_dtype
  *   block_table int32 [batch, max_blocks_per_seq], ctx_len int32 [batch],
  *   cu_new int32 [batch + 1], not decreasing, from >= 0 to <= n_rows

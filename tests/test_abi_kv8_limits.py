@@ -1,0 +1,31 @@
+"""Calls over the 8-bit cache and of the log probabilities that have to be refused, and what the binding
+asks of its tensors (no GPU needed: every case ends before any device work)."""
+import ctypes
+
+import pytest
+
+import verify_step_b200 as sd
+from verify_step_b200 import build as B
+
+A = 4096  # an aligned non-null address that is never read
+BAD, UNSUP = sd.SD_ERR_INVALID_ARG, sd.SD_ERR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return sd.lib()
+
+
+@pytest.mark.parametrize("cache", [sd.SD_E4M3, sd.SD_BF16])
+def test_queries_turned_in_place_need_one_row_stride(L, cache):
+    """Rows of one stride would be written over rows of the other that are still to be read."""
+    d = sd.AppendDesc(batch=2, n_new=3, n_rows=6, h_q=8, h_kv=2, head_dim=128, block_size=16,
+                      max_blocks_per_seq=4, num_blocks=8, ld_k=256, ld_v=256, ld_q=1024,
+                      ld_q_out=2048, dtype=sd.SD_BF16, cache_dtype=cache)
+    r = sd.Rotary(A, 128, sd.SD_ROPE_HALF, 1.0)
+    call = lambda: L.sd_append_kv(ctypes.byref(d), ctypes.byref(r), A, A, A, A, A, A, A, A, A, None, A,
+                                  None)
+    assert call() == BAD
+    d.ld_q, d.ld_q_out = 2048, 1024
+    assert call() == BAD

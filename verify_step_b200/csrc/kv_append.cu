@@ -825,6 +825,7 @@ static sd_status run_append(const sd_append_desc *d, const sd_rotary *rot, const
   if (d->n_rows == 0) return SD_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !table || !ctx_len) return SD_ERR_INVALID_ARG;
   if (d->h_q > 0 && (!q || !q_out)) return SD_ERR_INVALID_ARG;
+  if (d->h_q > 0 && q == q_out && d->ld_q != d->ld_q_out) return SD_ERR_INVALID_ARG;
   bool vec = vector_pairs(p.rot, p.D, V) && d->ld_k % V == 0 && d->ld_v % V == 0 &&
              aligned16(k_new) && aligned16(v_new) && aligned16(k_cache) && aligned16(v_cache);
   if (d->h_q > 0)

@@ -453,8 +453,8 @@ sd_status sd_rope(const sd_rope_desc *desc, const sd_rotary *rot, const void *x,
  *     rounded a second time.  Rolled-back rows count until the block is begun again.
  * Elements that are not finite do not count for s; infinities become +-448 s, NaN stays NaN.
  *   k_scale, v_scale float32 [num_blocks, h_kv] (unused otherwise, NULL ok)
- * Needs head_dim 64, 128, 256 or 512, block_size a multiple of 16, rot_dim a multiple of 16, all
- * row pointers 16-byte aligned and row strides a multiple of 16 bytes.
+ * Needs head_dim 64, 128, 256 or 512, block_size a multiple of 16 with block_size * head_dim < 2^31,
+ * rot_dim a multiple of 16, all row pointers 16-byte aligned and row strides a multiple of 16 bytes.
  *
  * The destination blocks must be allocated in block_table, and no block may receive rows of two
  * sequences in one call.  A block id out of range or a position beyond the table is skipped and

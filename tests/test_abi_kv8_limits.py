@@ -29,3 +29,16 @@ def test_queries_turned_in_place_need_one_row_stride(L, cache):
     assert call() == BAD
     d.ld_q, d.ld_q_out = 2048, 1024
     assert call() == BAD
+
+
+def test_blocks_whose_elements_do_not_fit_32_bits_are_refused(L):
+    d = sd.AppendDesc(batch=1, n_new=1, n_rows=1, h_kv=1, head_dim=64, block_size=1 << 25,
+                      max_blocks_per_seq=1, num_blocks=1, ld_k=64, ld_v=64, dtype=sd.SD_BF16,
+                      cache_dtype=sd.SD_E4M3)
+    call = lambda: L.sd_append_kv(ctypes.byref(d), None, A, A, None, A, A, A, A, A, A, None, None, None)
+    assert call() == UNSUP
+    d.head_dim, d.ld_k, d.ld_v, d.block_size = 512, 512, 512, 1 << 22
+    assert call() == UNSUP
+    d.n_rows = d.n_new = 0
+    d.block_size = 1 << 21
+    assert call() == sd.SD_OK

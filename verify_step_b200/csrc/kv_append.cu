@@ -821,6 +821,8 @@ static sd_status run_append(const sd_append_desc *d, const sd_rotary *rot, const
     if (!(d->head_dim == 64 || d->head_dim == 128 || d->head_dim == 256 || d->head_dim == 512) ||
         d->block_size % 16 || (rot != nullptr && rot->rot_dim % 16))
       return SD_ERR_UNSUPPORTED;
+    // a block's elements are counted in 32 bits
+    if ((long long)d->block_size * d->head_dim >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
   }
   if (d->n_rows == 0) return SD_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !table || !ctx_len) return SD_ERR_INVALID_ARG;

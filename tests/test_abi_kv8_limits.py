@@ -42,3 +42,61 @@ def test_blocks_whose_elements_do_not_fit_32_bits_are_refused(L):
     d.n_rows = d.n_new = 0
     d.block_size = 1 << 21
     assert call() == sd.SD_OK
+
+
+class OnDevice:
+    """A contiguous CUDA tensor as far as the binding looks."""
+    is_cuda = True
+
+    def __init__(self, device):
+        self.device, self.asked = device, False
+
+    def get_device(self):
+        self.asked = True
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 30
+
+    def data_ptr(self):
+        return A
+
+    def element_size(self):
+        return 1
+
+
+CALLS = {  # a call of n tensors, whose empty descriptor is refused by the library
+    "sd_rope_freqs": (lambda t: sd.sd_rope_freqs(sd.RopeFreqDesc(), t[0]), 1),
+    "sd_rope": (lambda t: sd.sd_rope(sd.RopeDesc(), turns(t[0]), *t[1:]), 5),
+    "sd_append_kv": (lambda t: sd.sd_append_kv(sd.AppendDesc(), turns(t[0]), *t[1:]), 12),
+    "sd_verify_attn_q8": (lambda t: sd.sd_verify_attn_q8(sd.AttnDesc(), *t), 9),
+    "sd_draft_xattn_q8": (lambda t: sd.sd_draft_xattn_q8(sd.AttnDesc(), *t), 10),
+    "sd_logprobs": (lambda t: sd.sd_logprobs(sd.LogprobsDesc(), *t), 7)}
+
+
+def turns(table):
+    r = sd.Rotary(A, 64, sd.SD_ROPE_HALF, 1.0)
+    r.table = table
+    return r
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_tensor_of_another_device_is_refused(L, monkeypatch, name):
+    """Whichever argument it is, the rotation's table and the workspace among them: the kernels of a
+    call run on the current device."""
+    monkeypatch.setattr(sd, "_current_device", lambda: 0)
+    monkeypatch.setattr(sd, "_stream", lambda s: 0)
+    monkeypatch.setattr(sd, "_nbytes", lambda t: 0)
+    call, n = CALLS[name]
+    good = [OnDevice(0) for _ in range(n)]
+    with pytest.raises(sd.SdError):  # the empty descriptor is refused, after the tensors
+        call(good)
+    assert all(t.asked for t in good)
+    for i in range(n):
+        t = [OnDevice(0) for _ in range(n)]
+        t[i] = OnDevice(1)
+        with pytest.raises(ValueError, match="current device"):
+            call(t)

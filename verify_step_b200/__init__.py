@@ -12,6 +12,7 @@ tensors (their data_ptr is used; they must be contiguous), descriptors as the ct
 structures below, ``stream`` as a torch.cuda.Stream (default: the current stream).
 Row tensors whose descriptor has a row stride (sd_rope, sd_append_kv) may be strided views whose
 rows are contiguous; a cache in 8 bits is a torch.float8_e4m3fn (or uint8) tensor.
+The calls from sd_rope_freqs on refuse tensors of another device than the current one.
 """
 from __future__ import annotations
 
@@ -188,23 +189,32 @@ def status_string(status: int) -> str:
     return lib().sd_status_string(int(status)).decode()
 
 
-def _ptr(t):
-    if t is None or isinstance(t, int):
-        return t
-    if t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
+def _refuse(t, dev):
+    """What is wrong with a tensor that _ptr or _rows_ptr does not take as it is."""
     if not t.is_cuda:
         raise ValueError("tensor arguments must live on a CUDA device")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError("tensors must live on the current device")
     raise ValueError("tensor arguments must be contiguous")
 
 
-def _rows_ptr(t, ld, rows, width):
+def _ptr(t, dev=None):
+    """Address of a contiguous CUDA tensor; with ``dev``, of that device (the current one, where the
+    call would run)."""
+    if t is None or isinstance(t, int):
+        return t
+    if (t.is_cuda if dev is None else t.get_device() == dev) and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dev)
+
+
+def _rows_ptr(t, ld, rows, width, dev=None):
     """Address of row data [rows, ...] whose rows of ``width`` elements are contiguous and ``ld``
     elements apart (a view of a wider buffer is fine)."""
     if t is None or isinstance(t, int):
         return t
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must live on a CUDA device")
+    if not (t.is_cuda if dev is None else t.get_device() == dev):
+        _refuse(t, dev)
     if t.is_contiguous() and t.numel() >= (rows - 1) * ld + width:
         return t.data_ptr()
     inner = 1
@@ -231,13 +241,6 @@ def _torch_cuda():
 
 def _current_device():
     return _torch_cuda()[0]()
-
-
-def _on_device(t):
-    """Refuses a tensor of another device than the current one, where the call would run."""
-    if (t is not None and not isinstance(t, int) and t.is_cuda
-            and t.get_device() != _current_device()):
-        raise ValueError("tensors must live on the current device")
 
 
 def _stream(stream):
@@ -335,7 +338,8 @@ def sd_linear(desc, x, w, out, table=None, tokens=None, token_sel=None, stream=N
 def sd_rope_freqs(desc, freqs, stream=None) -> float:
     """Fills ``freqs`` (int64 [rot_dim / 2]: 64-bit fractions of a turn); returns the amplitude."""
     amp = ctypes.c_float(1.0)
-    _check("sd_rope_freqs", lib().sd_rope_freqs(ctypes.byref(desc), _ptr(freqs), ctypes.byref(amp),
+    at = _ptr(freqs, _current_device())
+    _check("sd_rope_freqs", lib().sd_rope_freqs(ctypes.byref(desc), at, ctypes.byref(amp),
                                                 _stream(stream)))
     return amp.value
 
@@ -347,27 +351,30 @@ def rotary(freqs, layout=SD_ROPE_HALF, amplitude=1.0) -> Rotary:
     return r
 
 
-def _ref(x):
-    return ctypes.byref(x) if x is not None else None
+def _rot(rot, dev):
+    if rot is None:
+        return None
+    _ptr(getattr(rot, "table", None), dev)
+    return ctypes.byref(rot)
 
 
 def sd_rope(desc, rot, x, pos, ctx_len, out, stream=None):
-    _on_device(x)
-    width = desc.heads * desc.head_dim
-    _check("sd_rope", lib().sd_rope(
-        ctypes.byref(desc), _ref(rot), _rows_ptr(x, desc.ld_x, desc.rows, width), _ptr(pos),
-        _ptr(ctx_len), _rows_ptr(out, desc.ld_out, desc.rows, width), _stream(stream)))
+    dev, width = _current_device(), desc.heads * desc.head_dim
+    args = (_rot(rot, dev), _rows_ptr(x, desc.ld_x, desc.rows, width, dev), _ptr(pos, dev),
+            _ptr(ctx_len, dev), _rows_ptr(out, desc.ld_out, desc.rows, width, dev))
+    _check("sd_rope", lib().sd_rope(ctypes.byref(desc), *args, _stream(stream)))
 
 
 def sd_append_kv(desc, rot, k_new, v_new, q, k_cache, v_cache, k_scale, v_scale, block_table,
                  ctx_len, cu_new=None, q_out=None, stream=None):
-    _on_device(k_new)
+    dev = _current_device()
     n, kv, w = desc.n_rows, desc.h_kv * desc.head_dim, desc.h_q * desc.head_dim
-    _check("sd_append_kv", lib().sd_append_kv(
-        ctypes.byref(desc), _ref(rot), _rows_ptr(k_new, desc.ld_k, n, kv),
-        _rows_ptr(v_new, desc.ld_v, n, kv), _rows_ptr(q, desc.ld_q, n, w), _ptr(k_cache),
-        _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(ctx_len),
-        _ptr(cu_new), _rows_ptr(q_out, desc.ld_q_out, n, w), _stream(stream)))
+    args = (_rot(rot, dev), _rows_ptr(k_new, desc.ld_k, n, kv, dev),
+            _rows_ptr(v_new, desc.ld_v, n, kv, dev), _rows_ptr(q, desc.ld_q, n, w, dev),
+            _ptr(k_cache, dev), _ptr(v_cache, dev), _ptr(k_scale, dev), _ptr(v_scale, dev),
+            _ptr(block_table, dev), _ptr(ctx_len, dev), _ptr(cu_new, dev),
+            _rows_ptr(q_out, desc.ld_q_out, n, w, dev))
+    _check("sd_append_kv", lib().sd_append_kv(ctypes.byref(desc), *args, _stream(stream)))
 
 
 def sd_verify_attn_q8_workspace_size(desc: AttnDesc) -> int:
@@ -376,10 +383,12 @@ def sd_verify_attn_q8_workspace_size(desc: AttnDesc) -> int:
 
 def sd_verify_attn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, out, ws,
                       stream=None):
-    _on_device(q)
-    _check("sd_verify_attn_q8", lib().sd_verify_attn_q8(
-        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_table), _ptr(ctx_len), _ptr(out), _ptr(ws), _nbytes(ws), _stream(stream)))
+    dev = _current_device()
+    args = (_ptr(q, dev), _ptr(k_cache, dev), _ptr(v_cache, dev), _ptr(k_scale, dev),
+            _ptr(v_scale, dev), _ptr(block_table, dev), _ptr(ctx_len, dev), _ptr(out, dev),
+            _ptr(ws, dev), _nbytes(ws))
+    _check("sd_verify_attn_q8",
+           lib().sd_verify_attn_q8(ctypes.byref(desc), *args, _stream(stream)))
 
 
 def sd_draft_xattn_q8_workspace_size(desc: AttnDesc) -> int:
@@ -388,11 +397,12 @@ def sd_draft_xattn_q8_workspace_size(desc: AttnDesc) -> int:
 
 def sd_draft_xattn_q8(desc, q, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, q_pos,
                       out, ws, stream=None):
-    _on_device(q)
-    _check("sd_draft_xattn_q8", lib().sd_draft_xattn_q8(
-        ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-        _ptr(block_table), _ptr(ctx_len), _ptr(q_pos), _ptr(out), _ptr(ws), _nbytes(ws),
-        _stream(stream)))
+    dev = _current_device()
+    args = (_ptr(q, dev), _ptr(k_cache, dev), _ptr(v_cache, dev), _ptr(k_scale, dev),
+            _ptr(v_scale, dev), _ptr(block_table, dev), _ptr(ctx_len, dev), _ptr(q_pos, dev),
+            _ptr(out, dev), _ptr(ws, dev), _nbytes(ws))
+    _check("sd_draft_xattn_q8",
+           lib().sd_draft_xattn_q8(ctypes.byref(desc), *args, _stream(stream)))
 
 
 def sd_logprobs_workspace_size(desc: LogprobsDesc) -> int:
@@ -401,10 +411,10 @@ def sd_logprobs_workspace_size(desc: LogprobsDesc) -> int:
 
 def sd_logprobs(desc, logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None,
                 ws=None, stream=None):
-    _on_device(logits)
-    _check("sd_logprobs", lib().sd_logprobs(
-        ctypes.byref(desc), _ptr(logits), _ptr(tokens), _ptr(logprob), _ptr(entropy),
-        _ptr(top_ids), _ptr(top_logprobs), _ptr(ws), _nbytes(ws), _stream(stream)))
+    dev = _current_device()
+    args = (_ptr(logits, dev), _ptr(tokens, dev), _ptr(logprob, dev), _ptr(entropy, dev),
+            _ptr(top_ids, dev), _ptr(top_logprobs, dev), _ptr(ws, dev), _nbytes(ws))
+    _check("sd_logprobs", lib().sd_logprobs(ctypes.byref(desc), *args, _stream(stream)))
 
 
 def sd_device_status_read(stream=None) -> int:

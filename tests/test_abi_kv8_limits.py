@@ -100,3 +100,19 @@ def test_every_tensor_of_another_device_is_refused(L, monkeypatch, name):
         t[i] = OnDevice(1)
         with pytest.raises(ValueError, match="current device"):
             call(t)
+
+
+def test_the_current_stream_without_torch_s_inner_calls(monkeypatch):
+    """Where a torch has no raw calls for the current device and stream, the public ones serve."""
+    import torch
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+
+    class Stream:
+        def __init__(self, device):
+            self.cuda_stream = 1000 + device
+
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(sd, "_cuda", None)
+    assert sd._current_device() == 3 and sd._stream(None) == 1003

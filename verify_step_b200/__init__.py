@@ -235,7 +235,10 @@ def _torch_cuda():
     if _cuda is None:
         import torch
         torch.cuda.current_device()  # initialises CUDA
-        _cuda = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        # the raw calls build no object; a torch without them has the public ones
+        _cuda = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                 getattr(torch._C, "_cuda_getCurrentRawStream",
+                         lambda device: torch.cuda.current_stream(device).cuda_stream))
     return _cuda
 
 

@@ -253,10 +253,10 @@ __global__ void __launch_bounds__(kThreads, 4) chunk_kernel(const __grid_constan
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const float *z = p.z + (size_t)row * p.ld;
   const int begin = chunk * p.chunk_logits, end = min(p.V, begin + p.chunk_logits);
-  float x[16];
-  load_tile<VEC>(z, begin, end, x);  // before the token: a row that is not scored is read in vain
   int token;
   if (!scored(p, row, token, p.chunks == 1)) return;
+  float x[16];
+  load_tile<VEC>(z, begin, end, x);  // behind the token: the memory of a row without one may be missing
   if (TOP && tid == 0) sel.count = 0;
   float m = kFloor, S = 0.f, A = 0.f;
   u64 bound = 1;        // keys below it are not gathered,

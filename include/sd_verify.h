@@ -498,8 +498,9 @@ sd_status sd_append_kv(const sd_append_desc *desc, const sd_rotary *rot, const v
  * a query makes its output row NaN); softmax
  * weights enter the second product as two e4m3 parts (8 bits), relative to the largest of each
  * 128 keys, and are accumulated in float32.  Key and value rows outside every query's range are
- * not read as numbers (any codes may stand there).  A NaN in a V row that some, not all queries
- * of the call attend to makes the whole output rows of those queries NaN.
+ * not read as numbers (any codes may stand there).  A NaN in a V row makes that column NaN for the
+ * queries that attend to it, and may make their whole output rows NaN where others do not attend
+ * to it; those stay clear of it.
  */
 size_t sd_verify_attn_q8_workspace_size(const sd_attn_desc *desc);
 sd_status sd_verify_attn_q8(const sd_attn_desc *desc, const void *q, const void *k_cache,

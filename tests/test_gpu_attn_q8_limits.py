@@ -107,3 +107,42 @@ def test_a_length_near_the_integer_limit_is_recorded(L):
     assert sd.sd_device_status_read() == sd.SD_ERR_DEVICE
     sd.sd_device_status_clear()
     assert np.all(got[0] == 0) and np.all(np.abs(got - want)[1] <= tol[1])
+
+
+# ---------------------------------------------------------------------------- row groups
+
+@pytest.mark.parametrize("L,n_q,hq,hkv,D,bs,window", [
+    ([700, 31, 0], 7, 8, 2, 512, 16, 40),      # 28 rows: groups of 14
+    ([513], 16, 4, 1, 512, 48, 3),             # 64 rows: three groups, a window inside a group's own
+    ([300, 2], 9, 5, 1, 256, 16, 130),         # 45 rows
+    ([129, 1000], 33, 1, 1, 64, 32, 20),       # 33 rows: 17 and 16
+    ([90], 64, 1, 1, 128, 16, 0)])
+def test_row_groups_with_windows(L, n_q, hq, hkv, D, bs, window):
+    held(Case(10 + D, L, n_q, hq, hkv, D, bs, window))
+
+
+@pytest.mark.parametrize("hq,hkv,D,window", [(40, 1, 512, 0), (50, 1, 128, 33), (64, 1, 64, 200),
+                                             (66, 2, 256, 16)])
+def test_row_groups_of_drafter_calls(hq, hkv, D, window):
+    held(Case(11, [700, 3, 0], 1, hq, hkv, D, 16, window, draft=True, q_pos=[705, 3, 1]))
+
+
+@pytest.mark.parametrize("n_q,hq,D,window", [(7, 4, 512, 0), (16, 4, 128, 0), (16, 4, 512, 20),
+                                             (9, 4, 256, 300)])
+def test_nan_with_several_row_groups(n_q, hq, D, window):
+    """A NaN in V makes its column NaN for every query that attends to the key, and nothing for the
+    others, whichever group a query is in."""
+    L = 200
+    for at in (L + n_q - 2, L + 2, L, max(0, L - window + 3) if window else 5):
+        c = Case(12, [L], n_q, hq, 1, D, 16, window)
+        want, tol = c.reference()
+        c.vc[c.table[0, at // 16], 0, at % 16, 5] = 0x7F
+        got = c.run()
+        for j in range(n_q):
+            t = L + j
+            sees = at <= t and (not window or at >= t - window + 1)
+            if sees:
+                assert np.all(np.isnan(got[0, j, :, 5])), (at, j)
+            else:
+                assert np.all(np.abs(got[0, j] - want[0, j]) <= tol[0, j]), (at, j)
+        assert status_ok()

@@ -489,7 +489,8 @@ __device__ __forceinline__ bool is_edge(const Params &p, const Walk &w, int j_fi
 }
 
 // V rows that no query attends to may hold any codes, and 0 * NaN is NaN: they are cleared.  A NaN that
-// only some queries attend to is cleared too, and the group's rows that see it are returned.  One
+// not every row of the group attends to is cleared too, and the rows that see it are returned (their
+// outputs become NaN as a whole; a NaN that every row of the group attends to takes its column).  One
 // warp, a row (or the part of one that a lane's 16 bytes each cover) at a time.
 template <int D, int NR>
 __device__ __forceinline__ uint32_t clean_v(const Params &p, const Walk &w, uint8_t *tile,

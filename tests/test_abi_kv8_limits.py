@@ -116,3 +116,16 @@ def test_the_current_stream_without_torch_s_inner_calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", Stream)
     monkeypatch.setattr(sd, "_cuda", None)
     assert sd._current_device() == 3 and sd._stream(None) == 1003
+
+
+def test_row_counts_at_the_integer_limit_are_refused(L):
+    """Rows are counted up to whole CTAs in 32 bits."""
+    r = sd.Rotary(A, 2, sd.SD_ROPE_HALF, 1.0)
+    n = (1 << 31) - 1
+    d = sd.RopeDesc(rows=n, heads=1, head_dim=2, ld_x=2, ld_out=2, dtype=sd.SD_BF16, rows_per_seq=1)
+    assert L.sd_rope(ctypes.byref(d), ctypes.byref(r), A, A, None, 2 * A, None) == UNSUP
+    e = sd.AppendDesc(batch=1, n_new=n, n_rows=n, h_kv=1, head_dim=2, block_size=16,
+                      max_blocks_per_seq=4, num_blocks=8, ld_k=2, ld_v=2, dtype=sd.SD_BF16,
+                      cache_dtype=sd.SD_BF16)
+    assert L.sd_append_kv(ctypes.byref(e), None, A, A, None, A, A, None, None, A, A, None, None,
+                          None) == UNSUP

@@ -37,6 +37,7 @@ namespace app {
 
 constexpr int kMaxThreads = 256;    // rows_kernel
 constexpr int kQuantThreads = 512;  // quant_kernel
+constexpr int kMaxRows = INT_MAX - kMaxThreads;  // rows are counted up to whole CTAs
 
 struct Rot {
   const unsigned long long *freqs;  // null: no rotation
@@ -824,6 +825,7 @@ static sd_status run_append(const sd_append_desc *d, const sd_rotary *rot, const
     // a block's elements are counted in 32 bits
     if ((long long)d->block_size * d->head_dim >= (1ll << 31)) return SD_ERR_UNSUPPORTED;
   }
+  if (d->n_rows > kMaxRows) return SD_ERR_UNSUPPORTED;
   if (d->n_rows == 0) return SD_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !table || !ctx_len) return SD_ERR_INVALID_ARG;
   if (d->h_q > 0 && (!q || !q_out)) return SD_ERR_INVALID_ARG;
@@ -920,6 +922,7 @@ sd_status sd_rope(const sd_rope_desc *d, const sd_rotary *rot, const void *x, co
   if (!app::rotary_ok(rot, d->head_dim)) return SD_ERR_INVALID_ARG;
   const int64_t row = (int64_t)d->heads * d->head_dim;
   if (d->ld_x < row || d->ld_out < row) return SD_ERR_INVALID_ARG;
+  if (d->rows > app::kMaxRows) return SD_ERR_UNSUPPORTED;
   if (d->rows == 0) return SD_OK;
   if (!x || !out || (!pos && !ctx_len) || (!pos && d->rows_per_seq < 1)) return SD_ERR_INVALID_ARG;
   if (x == out && d->ld_x != d->ld_out) return SD_ERR_INVALID_ARG;

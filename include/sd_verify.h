@@ -495,9 +495,9 @@ sd_status sd_append_kv(const sd_append_desc *desc, const sd_rotary *rot, const v
  *
  * Scores are exact products of the bf16 query and the e4m3 keys, accumulated in float32 (query
  * elements below 2^-13 of their row's largest are rounded, by at most 2^-21 of it; an infinity in
- * a query makes its output row NaN); softmax
- * weights enter the second product as two e4m3 parts (8 bits), relative to the largest of each
- * 128 keys, and are accumulated in float32.  Key and value rows outside every query's range are
+ * a query makes its output row NaN).  Softmax weights enter the second product as two e4m3 parts:
+ * a weight is off by at most 2^-8 + 2^-12 of it or by 2^-22 of the largest among its 128 keys,
+ * whichever is more; their sums and the outputs are held in float32.  Key and value rows outside every query's range are
  * not read as numbers (any codes may stand there).  A NaN in a V row makes that column NaN for the
  * queries that attend to it, and may make their whole output rows NaN where others do not attend
  * to it; those stay clear of it.

@@ -2,6 +2,8 @@
 those of test_gpu_attn_q8, without its constant 1e-30 where outputs are small; a bf16 output below
 2^-126 is off by half its fixed step, 2^-134.
 """
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -93,6 +95,26 @@ def test_keys_of_zeros_under_large_scales():
     c.q = (c.q.double() * 2.0 ** 120).bfloat16()
     c.kc[:] = 0
     c.ks[:] = 2.0 ** 60
+    held(c)
+
+
+def test_a_key_of_nearly_all_weight_whose_value_is_zero():
+    """What is left of the output are the light keys of its tile, 2^-12 to 2^-20 of it each: a weight is
+    off by the larger of 2^-8 of it and 2^-22 of the tile's largest."""
+    D, L = 128, 120
+    c = Case(8, [L], 1, 1, 1, D, 16)
+    one = torch.tensor([1.0]).to(torch.float8_e4m3fn).view(torch.uint8)[0]
+    light = np.exp2(-12 - 8 * np.arange(L + 1) / L)
+    c.kc[:] = 0
+    c.vc[:] = one
+    c.ks[:] = c.vs[:] = 1.0
+    c.q[:] = 0
+    # key 0 scores 0, the others -12 ln 2: their scale spreads them down to -20 ln 2
+    c.q[0, 0, 0, 0] = 12 * math.log(2) / c.desc.scale
+    for p in range(1, L + 1):
+        c.kc[c.table[0, p // 16], 0, p % 16, 0] = one | 0x80
+        c.ks[c.table[0, p // 16]] = 1 + (p // 16) / 12
+    c.vc[c.table[0, 0], 0, 0] = 0
     held(c)
 
 

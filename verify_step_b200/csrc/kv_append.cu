@@ -20,7 +20,8 @@
 // writer.  It goes from head to head, the next head's rows in flight while this one's maximum is
 // joined; a thread has the same elements of every head and keeps their sines and cosines in shared
 // memory.  Bound by issue slots and latency, not by HBM: 54.4 us for 190 MB (3.5 TB/s, blocks of 16
-// rows, 4 heads of 512 elements), 48 without a rotation; leaving out the stores alone changed nothing.
+// rows, 4 heads of 512 elements), 48 without a rotation (V, never turned, is half of the work and goes
+// through the same unpacking and float maxima as K); leaving out the stores alone changed nothing.
 // Staging a block's rows in shared memory and going over them twice took 61 us, with copies a block
 // ahead 59, and with loops in place of unrolled heads 81.
 #include <cuda_fp8.h>

@@ -28,7 +28,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kTileLogits = 16 * kThreads;
-constexpr int kCap = 1024;  // gathered keys; a tile that brings more (rising logits) is searched by bits
+constexpr int kCap = 1024;  // gathered keys; a tile that brings more (rising logits) is gathered again, 256
+                            // keys at a time with thinning in between
 constexpr int kHigh = 512;  // more than these after a tile are thinned out
 constexpr int kDump = 64;   // keys that a chunk leaves for the merge, in any order
 

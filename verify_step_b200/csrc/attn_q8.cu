@@ -34,10 +34,10 @@
 // that a second kernel joins in CTA order.
 //
 // Measured (floor at the copy rate of 6.54 TB/s): 8 sequences of 16384 keys, 4 kv heads of 512, one query
-// row a head 89 us (82), three 94 us (82); 64 ragged sequences of up to 16384 keys at D 256 179 us
-// (146); one window of 514 keys, 2 kv heads of 256, 14.4 us, all latency.  At D 512 HBM bounds it.  Below,
-// the copy warp does: looking up and issuing the boxes of 128 keys takes it 1.4 us at pages of 16 rows
-// whatever D is (D 128 at 16 x 16384 keys: 2.5 to 2.8 TB/s).  Code is kept short in every role (eight
+// row a head 87 us (82), three 94 us (82); 64 ragged sequences of up to 16384 keys at D 256 177 to 187
+// us (146); one window of 514 keys, 2 kv heads of 256, 13.5 us, all latency.  At D 512 HBM bounds it.
+// Below, the copy warp does: looking up and issuing the boxes of 128 keys takes it 1.4 us at pages of 16
+// rows whatever D is (D 128 at 16 x 16384 keys: 2.7 to 3.0 TB/s).  Code is kept short in every role (eight
 // rows a thread, loops): they share the instruction cache, and unrolling made them slower.
 #include <algorithm>
 #include <climits>

@@ -19,7 +19,7 @@
 // The append to an e4m3 cache: a CTA owns one (block, heads, K or V), so the block's scale has one
 // writer.  It goes from head to head, the next head's rows in flight while this one's maximum is
 // joined; a thread has the same elements of every head and keeps their sines and cosines in shared
-// memory.  Bound by issue slots and latency, not by HBM: 54.4 us for 190 MB (3.5 TB/s, blocks of 16
+// memory.  Bound by issue slots and latency, not by HBM: 53.5 us for 190 MB (3.6 TB/s, blocks of 16
 // rows, 4 heads of 512 elements), 48 without a rotation (V, never turned, is half of the work and goes
 // through the same unpacking and float maxima as K); leaving out the stores alone changed nothing.
 // Staging a block's rows in shared memory and going over them twice took 61 us, with copies a block
